@@ -379,6 +379,129 @@ skv_status merge_state(const void* o_parts, const float* lse_parts, void* out, f
                        int64_t part_stride_o, int64_t part_stride_lse, skv_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* rope_apply: rotary positions of q and k, or their transpose (gradient).   */
+/*
+ * Pair i of every head row at position p turns by t = p * inv_freq[i]:
+ *   (x, y) -> factor * (x cos t - y sin t, x sin t + y cos t),
+ * i < rotary_dim / 2; dimensions >= rotary_dim are copied.  interleaved = 0:
+ * pairs (i, i + rotary_dim / 2); 1: pairs (2i, 2i + 1).  inverse = 1 applies
+ * the transpose (t -> -t, same factor): the gradient of the inputs given that
+ * of the outputs.  Angles are formed in fp64 (exact turns at any int32
+ * position), values turn in fp32 and are rounded once.
+ *
+ * q [B, Hq, S, D] / [B, S, Hq, D] / [T, Hq, D] in `layout` (TND: B = 1 and
+ * S = T); k likewise with Hkv, or NULL with k_out = NULL and Hkv = 0; outputs
+ * like the inputs, which they may be (in place) but not overlap otherwise.
+ * positions: device int32 [B, S] (TND: [T]).  inv_freq: device fp64
+ * [rotary_dim / 2], radians per position (rope_inv_freq).  bf16 or fp16.
+ * Errors: SKV_ERR_INVALID_ARG for NULL or misaligned pointers (inv_freq: 8
+ * bytes), bad sizes, an odd rotary_dim or one above D, overlap;
+ * SKV_ERR_UNSUPPORTED for fp32, or D or rotary_dim not a multiple of 16. */
+skv_status rope_apply(const void* q, const void* k, void* q_out, void* k_out, const int32_t* positions,
+                      const double* inv_freq, int B, int Hq, int Hkv, int S, int D, int rotary_dim, float factor,
+                      skv_dtype dtype, skv_layout layout, int interleaved, int inverse, skv_stream_t stream);
+
+/* Frequencies for rope_apply (host, fp64): inv_freq[i] for i < rotary_dim / 2
+ * and the factor on the rotated values (1 except for YARN).
+ *   NONE    base^(-2i / rotary_dim)
+ *   LINEAR  that / factor (positions interpolated)
+ *   NTK     base -> base * factor^(rotary_dim / (rotary_dim - 2))
+ *   YARN    f (1 - g) + f / factor g with g rising from 0 to 1 between the
+ *           pairs that turn beta_fast and beta_slow times over original_len
+ *           positions (Peng et al., "YaRN", 2023); factor 0.1 ln(factor) + 1.
+ * factor >= 1 (ignored for NONE); original_len, beta_* are read for YARN only. */
+typedef enum { SKV_ROPE_NONE = 0, SKV_ROPE_LINEAR = 1, SKV_ROPE_NTK = 2, SKV_ROPE_YARN = 3 } skv_rope_scaling;
+skv_status rope_inv_freq(int rotary_dim, double base, skv_rope_scaling scaling, double factor, int original_len,
+                         double beta_fast, double beta_slow, double* inv_freq, double* attn_factor);
+
+/* ------------------------------------------------------------------------ */
+/* The 8-bit key/value cache.                                                */
+/*
+ * codes [B, Hkv, capacity, D], one byte each, 16-byte aligned, contiguous;
+ * scale fp32 [B, Hkv, capacity / block], >= 0; a value is code * scale.  block
+ * (tokens per scale) is 16, 32, 64 or 128 and divides capacity; D is 64, 128 or
+ * 256.  Nothing needs initialising: what lies behind a sequence's last token is
+ * never used, and stays as it is.  Codes must be finite (no e4m3 NaN) where
+ * tokens are. */
+typedef enum { SKV_INT8 = 0, SKV_E4M3 = 1 } skv_code;
+
+/* kv8_append: quantises new tokens into the cache.
+ *
+ * Token i of sequence b goes to position start[b] + i.  In each block it
+ * touches, with a the largest |x| of the block's new tokens and s_old the scale
+ * of tokens already in it (0 if it begins at or behind start[b]):
+ *   s = max(a / qmax, s_old), qmax = 127 or 448;  code = rne(x * (1 / s)), and
+ * where s > s_old the older codes c become rne((c * s_old) * (1 / s)), all in
+ * fp32.  s < 2^-126 is stored as 0 with codes 0.  A NaN or infinity makes its
+ * block's scale non-finite and its codes 0, so that all of it reads as NaN.
+ *
+ * k_new, v_new: [B, Hkv, S, D] / [B, S, Hkv, D], or TND [T, Hkv, D] with
+ * cu_seqlens [B + 1] and S = the longest sequence.  num_new: device int32 [B]
+ * or NULL (= S), dense layouts only: the first num_new[b] tokens of b are
+ * appended.  start, num_new and lengths are read on the device and clamped
+ * (start to [0, capacity], counts to [0, S]); tokens that do not fit the
+ * capacity are dropped.  Two sequences are never the same cache row, so calls
+ * need no order among batch entries; appends to one cache must not overlap. */
+skv_status kv8_append(const void* k_new, const void* v_new, void* k_codes, void* v_codes, float* k_scale,
+                      float* v_scale, const int32_t* start, const int32_t* num_new, const int32_t* cu_seqlens, int B,
+                      int Hkv, int S, int T, int capacity, int D, int block, skv_dtype dtype, skv_code codes,
+                      skv_layout layout, skv_stream_t stream);
+
+/* kv8_fetch: a window of the cache in 16 bits (for attention over a cached
+ * prefix with attn_fwd_lse): out[b, h, i] = code * scale at position
+ * start[b] + i, i < n; 0 where that is not in [0, kv_len[b]).  start, kv_len:
+ * device int32 [B] or NULL (0, capacity).  k_out, v_out [B, Hkv, n, D] (HND) or
+ * [B, n, Hkv, D] (NHD), bf16 or fp16. */
+skv_status kv8_fetch(const void* k_codes, const void* v_codes, const float* k_scale, const float* v_scale, void* k_out,
+                     void* v_out, const int32_t* start, const int32_t* kv_len, int B, int Hkv, int n, int capacity,
+                     int D, int block, skv_dtype dtype, skv_code codes, skv_layout layout, skv_stream_t stream);
+
+/* attn_splitkv_decode_kv8: attn_splitkv_decode over the 8-bit cache.
+ *
+ * O, LSE, kv_len, causal (as attn_splitkv_decode_causal), num_splits and the
+ * split rule are those of attn_splitkv_decode with K = codes * scale and
+ * V = codes * scale; the products take the codes exactly.  A non-finite scale
+ * makes the rows that see its block NaN.
+ * weights: device fp32 [B, Hkv, capacity] (16-byte aligned) or NULL.  If given,
+ * each visible key's attention weight is added to it: weights[b, h, j] += sum
+ * over the G * Lq query rows of kv head h of exp(s_j) / sum exp(s), one addition
+ * per entry and call; entries >= kv_len[b] stay as they are.
+ * workspace: device, 256-byte aligned, >= attn_splitkv_kv8_workspace(...) bytes
+ * for the split count used (with weights: the rows' logits, 4 * B * Hq * Lq *
+ * capacity bytes). */
+skv_status attn_splitkv_decode_kv8(const void* q, const void* k_codes, const void* v_codes, const float* k_scale,
+                                   const float* v_scale, void* out, float* lse, float* weights, int B, int Hq, int Hkv,
+                                   int Lq, int capacity, int D, int block, float scale, skv_dtype dtype,
+                                   skv_code codes, const int32_t* kv_len, int causal, int num_splits, void* workspace,
+                                   size_t workspace_bytes, skv_stream_t stream);
+
+/* Split count of the 8-bit decode (host): requested_splits if > 0, else as many
+ * as give about two CTAs per SM over the B * Hkv * ceil(G * Lq / 16) units of
+ * one split, with at least 128 keys each (the kernel's CTAs come two to an SM). */
+skv_status attn_splitkv_kv8_plan(int B, int Hq, int Hkv, int Lq, int capacity, int D, int num_sms,
+                                 int requested_splits, int* num_splits);
+size_t attn_splitkv_kv8_workspace(int B, int Hq, int Lq, int capacity, int D, int num_splits, int weights);
+
+/* kv8_evict: cuts each sequence to `budget` tokens by accumulated weight.
+ *
+ * With n = kv_len[b] (NULL: capacity; clamped to [0, capacity]) tokens and
+ * n > budget, each head keeps its first `sink`, its last `recent` and, of those
+ * between, the budget - sink - recent with the largest weights (equal weights:
+ * the lowest position; NaN counts below all); else all n.  Kept tokens move in
+ * order into the other cache (to_*, same B, Hkv, D, block and codes; capacity
+ * to_capacity >= budget), which must not overlap this one.  Each block's scale
+ * there is the largest of its tokens' scales s_j, codes rne((c * s_j) * (1 / s)),
+ * unchanged where s_j = s.  to_weights [B, Hkv, to_capacity] gets the kept
+ * weights, kept int32 [B, Hkv, budget] the kept positions (-1 behind the last),
+ * new_len int32 [B] = min(n, budget) (may not be kv_len).  What lies behind the
+ * last kept token stays as it was. */
+skv_status kv8_evict(const void* k_codes, const void* v_codes, const float* k_scale, const float* v_scale,
+                     const float* weights, const int32_t* kv_len, void* to_k_codes, void* to_v_codes,
+                     float* to_k_scale, float* to_v_scale, float* to_weights, int32_t* kept, int32_t* new_len, int B,
+                     int Hkv, int capacity, int to_capacity, int D, int block, skv_code codes, int budget, int sink,
+                     int recent, skv_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* Diagnostics.                                                              */
 
 /* Static text for a status code. */

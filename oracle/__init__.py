@@ -39,6 +39,7 @@ __all__ = [
     "kv_mean", "smooth_shift", "smoothed_attention_rows", "chunked",
     "split_bounds", "auto_num_splits", "varlen_schedule", "lse_varlen_to_dense",
     "causal_key_counts", "quantize_int8_blocks", "int8_attention_rows", "INT8_BLOCK",
+    "rope", "round_e4m3", "kv8_append", "key_weights", "kv8_kept", "kv8_move", "KV8_QMAX",
 ]
 
 
@@ -427,3 +428,137 @@ def varlen_schedule(cu_seqlens_q, cu_seqlens_k, H: int, rows_per_cta: int = PREF
             for i in range(nblk):
                 items.append((b, h, i))
     return order, offsets, items
+
+
+# ---------------------------------------------------------------------------
+# Rotary positions and the 8-bit cache (not on the source pages: definitions
+# of include/splitkv.h).
+# ---------------------------------------------------------------------------
+
+def rope(x, positions, inv_freq, layout: str = "HND", interleaved: bool = False, factor: float = 1.0,
+         inverse: bool = False) -> np.ndarray:
+    """Rotary positions in fp64: pair i turns by positions * inv_freq[i]; pairs
+    (2i, 2i + 1) or (i, i + R / 2) of the first R = 2 len(inv_freq) dimensions,
+    the rest copied; inverse turns back (times the same factor)."""
+    y = to_f64(x).copy()
+    f = np.asarray(to_f64(inv_freq))
+    t = np.asarray(to_f64(positions))[..., None] * f * (-1.0 if inverse else 1.0)
+    heads_at = {"HND": 1, "NHD": 2, "TND": 1}[layout]
+    c, s = (np.expand_dims(factor * g(t), heads_at) for g in (np.cos, np.sin))
+    R = 2 * f.shape[0]
+    first, second = (slice(0, R, 2), slice(1, R, 2)) if interleaved else (slice(0, R // 2), slice(R // 2, R))
+    a, b = y[..., first].copy(), y[..., second].copy()
+    y[..., first], y[..., second] = a * c - b * s, a * s + b * c
+    return y
+
+
+def round_e4m3(x) -> np.ndarray:
+    """Nearest e4m3 value, ties to even, saturating at 448 (3 mantissa bits,
+    smallest normal 2^-6, steps of 2^-9 below it)."""
+    x = np.asarray(x, dtype=np.float64)
+    mag = np.maximum(np.abs(x), 2.0 ** -6)
+    step = 2.0 ** (np.floor(np.log2(mag)) - 3)
+    return np.clip(np.rint(x / step) * step, -448.0, 448.0)
+
+
+KV8_QMAX = {"int8": 127.0, "e4m3": 448.0}
+
+
+def _kv8_inverse(s: np.float32) -> np.float32:
+    return np.float32(1.0) / s if s > 0 and np.isfinite(s) else np.float32(0.0)
+
+
+def _kv8_codes(x32: np.ndarray, inv: np.float32, codes: str) -> np.ndarray:
+    y = (x32 * inv).astype(np.float32)
+    return np.rint(y).astype(np.float64) if codes == "int8" else round_e4m3(y)
+
+
+def kv8_append(k_codes: np.ndarray, k_scale: np.ndarray, new, start: int, count: int, block: int,
+               codes: str) -> None:
+    """Appends count tokens (new [>= count, D]) at `start` to one head's codes
+    [capacity, D] (their values) and scales [capacity / block], in place.
+
+    Per touched block: s = max(a / qmax, s_old) over the new tokens' largest
+    magnitude a and the scale of older tokens in the block; codes rne(x * (1/s));
+    older codes rne((c * s_old) * (1/s)) where s grew; all in fp32.  s < 2^-126
+    is 0 with codes 0; a non-finite s has codes 0."""
+    capacity = k_codes.shape[0]
+    end = min(start + count, capacity)
+    x = np.asarray(to_f64(new), dtype=np.float32)
+    if end <= start:
+        return
+    with np.errstate(all="ignore"):
+        for blk in range(start // block, (end - 1) // block + 1):
+            lo, hi = max(blk * block, start), min((blk + 1) * block, end)
+            fresh = x[lo - start: hi - start]
+            a = np.max(np.abs(fresh)) if np.all(~np.isnan(fresh)) else np.float32(np.nan)
+            t = np.float32(a) / np.float32(KV8_QMAX[codes])
+            s_old = np.float32(k_scale[blk]) if blk * block < start else np.float32(0.0)
+            s = t if (t > s_old or np.isnan(t)) else s_old
+            if s < np.float32(2.0 ** -126):
+                s = np.float32(0.0)
+            good = bool(s < np.inf)
+            inv = _kv8_inverse(s)
+            k_codes[lo:hi] = _kv8_codes(fresh, inv, codes) if good else 0.0
+            if blk * block < start and (s > s_old or (not good and s_old < np.inf)):
+                old = slice(blk * block, start)
+                held = (k_codes[old].astype(np.float32) * s_old).astype(np.float32)
+                k_codes[old] = _kv8_codes(held, inv, codes) if good else 0.0
+            k_scale[blk] = s
+
+
+def key_weights(q, k, scale: float, lengths: Sequence[int], causal: bool = False) -> np.ndarray:
+    """Each key's attention weight summed over the query rows of its kv head:
+    [B, Hkv, L] from q [B, Hq, Lq, D], k [B, Hkv, L, D]; lengths are the keys of
+    each batch entry (causal: row i of Lq sees the first length - Lq + 1 + i)."""
+    q, k = to_f64(q), to_f64(k)
+    B, Hq, Lq, _ = q.shape
+    Hkv, L = k.shape[1], k.shape[2]
+    G = Hq // Hkv
+    w = np.zeros((B, Hkv, L))
+    for b in range(B):
+        for h in range(Hq):
+            for i in range(Lq):
+                n = max(lengths[b] - Lq + 1 + i, 0) if causal else lengths[b]
+                if n == 0:
+                    continue
+                x = scale * (k[b, h // G, :n] @ q[b, h, i])
+                p = np.exp(x - x.max())
+                w[b, h // G, :n] += p / p.sum()
+    return w
+
+
+def kv8_kept(weights, n: int, budget: int, sink: int, recent: int) -> np.ndarray:
+    """Positions kv8_evict keeps of one head's n tokens, in order: the first
+    `sink`, the last `recent`, and the heaviest of the rest (ties: the lowest
+    position; NaN below all)."""
+    if n <= budget:
+        return np.arange(n)
+    w = np.asarray(to_f64(weights))
+    middle = list(range(sink, n - recent))
+    # NaN last, then by weight from the top, then by position
+    middle.sort(key=lambda j: (np.isnan(w[j]), 0.0 if np.isnan(w[j]) else -w[j], j))
+    chosen = middle[: budget - sink - recent]
+    return np.array(sorted(list(range(sink)) + chosen + list(range(n - recent, n))), dtype=np.int64)
+
+
+def kv8_move(k_codes: np.ndarray, k_scale: np.ndarray, kept: np.ndarray, block: int,
+             codes: str) -> Tuple[np.ndarray, np.ndarray]:
+    """Codes [len(kept), D] and block scales of the kept tokens of one head: a
+    block's scale is the largest of its tokens', codes rne((c * s_j) * (1 / s))."""
+    s_tok = np.asarray(k_scale, dtype=np.float32)[kept // block]
+    out = np.zeros((len(kept), k_codes.shape[1]))
+    scales = np.zeros((len(kept) + block - 1) // block, dtype=np.float32)
+    with np.errstate(all="ignore"):
+        for blk in range(len(scales)):
+            at = slice(blk * block, min((blk + 1) * block, len(kept)))
+            st = s_tok[at]
+            s = np.float32(np.nan) if np.any(np.isnan(st)) else st.max()
+            if s < np.float32(2.0 ** -126):
+                s = np.float32(0.0)
+            held = (k_codes[kept[at]].astype(np.float32) * st[:, None]).astype(np.float32)
+            moved = _kv8_codes(held, _kv8_inverse(s), codes) if s < np.inf else np.zeros(held.shape)
+            same = (st == s)[:, None]
+            out[at] = np.where(same, k_codes[kept[at]], moved)
+            scales[blk] = s
+    return out, scales

@@ -13,14 +13,19 @@ Entry points (same names as the C ABI):
 * ``attn_fwd_lse_chunks`` the partials of several KV chunks in one launch (for merge_state)
 * ``attn_splitkv_decode`` split-KV decode (stable per-split online softmax)
 * ``merge_state``         merge partial (O, LSE) pairs of disjoint KV ranges
+* ``rope_inv_freq``, ``rope_apply``   rotary positions of q and k (and their transpose)
+* ``kv8_cache``, ``kv8_append``, ``kv8_fetch``   a key/value cache in 8 bits with block scales
+* ``attn_splitkv_decode_kv8``   split-KV decode over that cache, with the keys' attention weights
+* ``kv8_evict``           cuts that cache to a budget by accumulated attention weight
 * ``attn_splitkv_plan``, ``attn_splitkv_workspace``, ``attn_splitkv_workspace_init``, ``attn_fwd_lse_workspace``,
   ``attn_varlen_plan``     host-side planning / sizing queries
 """
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
-from typing import Optional, Sequence, Tuple
+from typing import NamedTuple, Optional, Sequence, Tuple
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libsplitkv.so")
@@ -28,9 +33,12 @@ LIB_PATH = os.path.join(HERE, "libsplitkv.so")
 SKV_OK, SKV_ERR_INVALID_ARG, SKV_ERR_UNSUPPORTED, SKV_ERR_WORKSPACE_TOO_SMALL, SKV_ERR_CUDA = range(5)
 DTYPES = {"bf16": 0, "fp16": 1, "fp32": 2}
 LAYOUTS = {"HND": 0, "NHD": 1, "TND": 2}
+CODES = {"int8": 0, "e4m3": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 # (name, restype, argtypes) of every exported symbol
 _c_int, _c_float, _c_size, _c_i64, _vp = ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_int64, ctypes.c_void_p
+_c_double = ctypes.c_double
 SIGNATURES = {
     "attn_fwd_lse": (_c_int, [_vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_float,
                               _c_int, _c_int, _vp, _vp, _c_int, _c_int, _c_int, _vp, _c_size, _vp]),
@@ -58,6 +66,15 @@ SIGNATURES = {
     "attn_splitkv_workspace_init": (_c_int, [_vp, _c_size, _vp]),
     "merge_state": (_c_int, [_vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int,
                              _c_i64, _c_i64, _vp]),
+    "rope_apply": (_c_int, [_vp] * 6 + [_c_int] * 6 + [_c_float] + [_c_int] * 4 + [_vp]),
+    "rope_inv_freq": (_c_int, [_c_int, _c_double, _c_int, _c_double, _c_int, _c_double, _c_double, _vp, _vp]),
+    "kv8_append": (_c_int, [_vp] * 9 + [_c_int] * 10 + [_vp]),
+    "kv8_fetch": (_c_int, [_vp] * 8 + [_c_int] * 9 + [_vp]),
+    "attn_splitkv_kv8_plan": (_c_int, [_c_int] * 8 + [_vp]),
+    "attn_splitkv_kv8_workspace": (_c_size, [_c_int] * 7),
+    "attn_splitkv_decode_kv8": (_c_int, [_vp] * 8 + [_c_int] * 7 + [_c_float, _c_int, _c_int, _vp, _c_int, _c_int, _vp,
+                                                                    _c_size, _vp]),
+    "kv8_evict": (_c_int, [_vp] * 13 + [_c_int] * 10 + [_vp]),
     "skv_status_string": (ctypes.c_char_p, [_c_int]),
     "skv_last_cuda_error": (_c_int, []),
     "skv_device_error": (_c_int, [_vp]),
@@ -173,6 +190,25 @@ def _workspace(nbytes: int, device, workspace):
     if workspace is None:
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
     return workspace, workspace.numel() * workspace.element_size()
+
+
+class _Here:
+    """A context that leaves the current device as it is."""
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE = _Here()
+
+
+def _on(device):
+    """Makes the tensors' device current for a call (launches go to the current device)."""
+    torch = _torch()
+    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
 
 # ------------------------------------------------------------------ queries
@@ -527,7 +563,288 @@ def merge_state(o_parts, lse_parts, layout: str = "HND", out=None, lse=None, out
     return out, lse
 
 
+# ------------------------------------------------------------------ rotary positions
+
+def rope_inv_freq(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                  original_len: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                  device="cuda") -> Tuple["object", float]:
+    """Frequencies for rope_apply: (inv_freq float64 [rotary_dim / 2] on `device`,
+    factor).  scaling: "none", "linear", "ntk" or "yarn" (original_len and the
+    betas are read for "yarn" only)."""
+    torch = _torch()
+    _expect(scaling in ROPE_SCALINGS, f"unknown scaling {scaling!r}")
+    out = (ctypes.c_double * max(int(rotary_dim) // 2, 1))()
+    m = ctypes.c_double(0.0)
+    _check(lib().rope_inv_freq(int(rotary_dim), float(base), ROPE_SCALINGS[scaling], float(factor), int(original_len),
+                               float(beta_fast), float(beta_slow), out, ctypes.byref(m)), "rope_inv_freq")
+    return torch.tensor(list(out), dtype=torch.float64, device=device), m.value
+
+
+def rope_apply(q, k, positions, inv_freq, layout: str = "HND", interleaved: bool = False, factor: float = 1.0,
+               inverse: bool = False, q_out=None, k_out=None, stream=None):
+    """Rotary positions of q [B,Hq,S,D] (HND), [B,S,Hq,D] (NHD) or [T,Hq,D] (TND)
+    and of k (likewise with Hkv; may be None), in one launch.
+
+    positions: int32 [B,S] (TND: [T]); inv_freq: float64 [R/2], R <= D dimensions
+    turn (D and R multiples of 16), the others are copied.  interleaved: pairs
+    (2i, 2i+1) instead of (i, i + R/2).  inverse: the transpose, i.e. the
+    gradient of the inputs given that of the outputs.  q_out=q, k_out=k work in
+    place.  Returns (q_out, k_out)."""
+    torch = _torch()
+    _expect(layout in LAYOUTS, f"unknown layout {layout!r}")
+    _expect(q.dim() == (3 if layout == "TND" else 4), f"{layout} q has {q.dim()} dimensions")
+    _consistent(q, {"k": k, "positions": positions, "inv_freq": inv_freq, "q_out": q_out, "k_out": k_out},
+                same_dtype=("k", "q_out", "k_out"), int32=("positions",))
+    _expect(inv_freq.dtype == torch.float64, f"inv_freq must be float64, got {inv_freq.dtype}")
+    _expect(inv_freq.dim() == 1, "inv_freq is [rotary_dim / 2]")
+    if layout == "HND":
+        B, Hq, S, D = q.shape
+    elif layout == "NHD":
+        B, S, Hq, D = q.shape
+    else:
+        B, (S, Hq, D) = 1, q.shape
+    Hkv = 0
+    if k is not None:
+        _expect(k.dim() == q.dim(), f"{layout} k has {k.dim()} dimensions")
+        Hkv = k.shape[1 if layout != "NHD" else 2]
+        _shape(k, {"HND": (B, Hkv, S, D), "NHD": (B, S, Hkv, D), "TND": (S, Hkv, D)}[layout], "k")
+    _shape(positions, (S,) if layout == "TND" else (B, S), "positions")
+    _shape(q_out, q.shape, "q_out")
+    _expect(k is not None or k_out is None, "k_out without k")
+    if k is not None:
+        _shape(k_out, k.shape, "k_out")
+    _need_cuda(q, k, positions, inv_freq, q_out, k_out)
+    if q_out is None:
+        q_out = torch.empty_like(q)
+    if k_out is None and k is not None:
+        k_out = torch.empty_like(k)
+    if S == 0:
+        return q_out, k_out
+    with _on(q.device):
+        st = lib().rope_apply(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), _ptr(positions), _ptr(inv_freq), B, Hq, Hkv,
+                              S, D, 2 * inv_freq.numel(), float(factor), _dtype_code(q), LAYOUTS[layout],
+                              int(bool(interleaved)), int(bool(inverse)), _stream(stream, q.device))
+    _check(st, "rope_apply")
+    return q_out, k_out
+
+
+# ------------------------------------------------------------------ 8-bit cache
+
+class KV8Cache(NamedTuple):
+    """A key/value cache in 8 bits: codes k, v [B,Hkv,capacity,D] (int8 or
+    float8_e4m3fn) and scales k_scale, v_scale float32 [B,Hkv,capacity/block].
+    A value is code * scale.  The calls below check the tensors."""
+    k: "object"
+    v: "object"
+    k_scale: "object"
+    v_scale: "object"
+
+
+def kv8_cache(B: int, Hkv: int, capacity: int, D: int, block: int = 64, codes: str = "int8", device="cuda") -> KV8Cache:
+    """A new, empty cache (uninitialised memory: nothing in it needs to be zero)."""
+    torch = _torch()
+    _expect(codes in CODES, f"unknown codes {codes!r}")
+    _expect(block in (16, 32, 64, 128) and capacity > 0 and capacity % block == 0,
+            f"capacity {capacity} must be a positive multiple of the block ({block}: one of 16, 32, 64, 128)")
+    dt = torch.int8 if codes == "int8" else torch.float8_e4m3fn
+    code = [torch.empty(B, Hkv, capacity, D, dtype=dt, device=device) for _ in range(2)]
+    scale = [torch.empty(B, Hkv, capacity // block, dtype=torch.float32, device=device) for _ in range(2)]
+    return KV8Cache(*code, *scale)
+
+
+def _kv8(cache, ref, what: str = "cache"):
+    """Checks a cache's tensors (on the device of `ref`): (B, Hkv, capacity, D, block, code)."""
+    torch = _torch()
+    k, v, ks, vs = cache
+    _expect(k.dim() == 4, f"{what}.k is [B, Hkv, capacity, D]")
+    _expect(k.dtype in (torch.int8, torch.float8_e4m3fn), f"{what}.k has dtype {k.dtype}")
+    _expect(v.dtype == k.dtype and v.shape == k.shape, f"{what}.v must be like {what}.k")
+    _expect(ks.dtype == torch.float32 and vs.dtype == torch.float32, f"{what} scales must be float32")
+    B, Hkv, capacity, D = k.shape
+    blocks = ks.shape[-1] if ks.dim() == 3 else 0
+    _expect(blocks > 0 and capacity % blocks == 0 and ks.shape == (B, Hkv, blocks) and vs.shape == ks.shape,
+            f"{what} scales are [B, Hkv, capacity / block]")
+    for t in cache:
+        _expect(t.device == ref.device, f"{what} is on {t.device}, expected {ref.device}")
+    _need_cuda(k, v, ks, vs)
+    return B, Hkv, capacity, D, capacity // blocks, 0 if k.dtype == torch.int8 else 1
+
+
+def kv8_append(cache: KV8Cache, k, v, start, num_new=None, layout: str = "HND", cu_seqlens=None,
+               max_seqlen: Optional[int] = None, stream=None) -> KV8Cache:
+    """Quantises new tokens into the cache, in place.
+
+    k, v: [B,Hkv,S,D] (HND), [B,S,Hkv,D] (NHD), or [T,Hkv,D] (TND, with int32
+    cu_seqlens [B+1] and max_seqlen).  Token i of sequence b goes to position
+    start[b] + i (int32 device tensor [B]); num_new: optional int32 [B], the
+    first num_new[b] tokens only (dense layouts).  Positions and counts are
+    clamped on the device; tokens behind the capacity are dropped.  A block's
+    scale grows with its largest value and its older codes follow."""
+    B, Hkv, capacity, D, block, code = _kv8(cache, k)
+    _expect(layout in LAYOUTS, f"unknown layout {layout!r}")
+    _consistent(k, {"v": v, "start": start, "num_new": num_new, "cu_seqlens": cu_seqlens}, same_dtype=("v",),
+                int32=("start", "num_new", "cu_seqlens"))
+    T = 0
+    if layout == "TND":
+        _expect(cu_seqlens is not None and max_seqlen is not None, "TND layout needs cu_seqlens and max_seqlen")
+        _expect(num_new is None, "TND lengths are those of cu_seqlens")
+        _expect(k.dim() == 3, "TND tensors are [tokens, heads, D]")
+        T, S = k.shape[0], int(max_seqlen)
+        _shape(k, (T, Hkv, D), "k")
+        _shape(cu_seqlens, (B + 1,), "cu_seqlens")
+    else:
+        _expect(cu_seqlens is None and max_seqlen is None, "cu_seqlens and max_seqlen belong to the TND layout")
+        _expect(k.dim() == 4, f"{layout} tensors are 4-D")
+        S = k.shape[2 if layout == "HND" else 1]
+        _shape(k, (B, Hkv, S, D) if layout == "HND" else (B, S, Hkv, D), "k")
+    _shape(v, k.shape, "v")
+    _expect(start is not None, "start is needed")
+    _shape(start, (B,), "start")
+    _shape(num_new, (B,), "num_new")
+    _need_cuda(k, v, start, num_new, cu_seqlens)
+    if k.numel() == 0:
+        return cache
+    with _on(k.device):
+        st = lib().kv8_append(_ptr(k), _ptr(v), _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scale), _ptr(cache.v_scale),
+                              _ptr(start), _ptr(num_new), _ptr(cu_seqlens), B, Hkv, S, T, capacity, D, block,
+                              _dtype_code(k), code, LAYOUTS[layout], _stream(stream, k.device))
+    _check(st, "kv8_append")
+    return cache
+
+
+def kv8_fetch(cache: KV8Cache, n: int, dtype=None, start=None, kv_len=None, layout: str = "HND", k_out=None, v_out=None,
+              stream=None):
+    """A window of n tokens of every sequence in 16 bits: (k, v) [B,Hkv,n,D] (HND)
+    or [B,n,Hkv,D] (NHD), token i from position start[b] + i (start: int32 device
+    tensor [B], default 0); zero at positions outside [0, kv_len[b])."""
+    torch = _torch()
+    B, Hkv, capacity, D, block, code = _kv8(cache, cache.k)
+    _expect(layout in ("HND", "NHD"), f"kv8_fetch takes HND or NHD, not {layout}")
+    _expect(n >= 0, "n must not be negative")
+    _consistent(cache.k, {"start": start, "kv_len": kv_len, "k_out": k_out, "v_out": v_out}, int32=("start", "kv_len"))
+    if dtype is None:
+        dtype = k_out.dtype if k_out is not None else torch.bfloat16
+    shape = (B, Hkv, n, D) if layout == "HND" else (B, n, Hkv, D)
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        _shape(t, shape, name)
+        _expect(t is None or t.dtype == dtype, f"{name} must be {dtype}")
+    _shape(start, (B,), "start")
+    _shape(kv_len, (B,), "kv_len")
+    _need_cuda(start, kv_len, k_out, v_out)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=dtype, device=cache.k.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=dtype, device=cache.k.device)
+    if n == 0:
+        return k_out, v_out
+    with _on(cache.k.device):
+        st = lib().kv8_fetch(_ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scale), _ptr(cache.v_scale), _ptr(k_out),
+                             _ptr(v_out), _ptr(start), _ptr(kv_len), B, Hkv, int(n), capacity, D, block,
+                             _dtype_code(k_out), code, LAYOUTS[layout], _stream(stream, cache.k.device))
+    _check(st, "kv8_fetch")
+    return k_out, v_out
+
+
+def attn_splitkv_kv8_plan(B: int, Hq: int, Hkv: int, Lq: int, capacity: int, D: int = 128, num_sms: int = 148,
+                          requested_splits: int = 0) -> int:
+    """Split count of attn_splitkv_decode_kv8."""
+    ns = ctypes.c_int(0)
+    _check(lib().attn_splitkv_kv8_plan(B, Hq, Hkv, Lq, capacity, D, num_sms, requested_splits, ctypes.byref(ns)),
+           "attn_splitkv_kv8_plan")
+    return ns.value
+
+
+def attn_splitkv_kv8_workspace(B: int, Hq: int, Lq: int, capacity: int, D: int, num_splits: int,
+                               weights: bool = False) -> int:
+    return int(lib().attn_splitkv_kv8_workspace(B, Hq, Lq, capacity, D, num_splits, int(bool(weights))))
+
+
+@functools.lru_cache(maxsize=256)
+def _kv8_plan(B, Hq, Hkv, Lq, capacity, D, requested, weights, device):
+    """(splits, workspace bytes): a function of the sizes and the device's SM count."""
+    sms = _torch().cuda.get_device_properties(device).multi_processor_count
+    splits = attn_splitkv_kv8_plan(B, Hq, Hkv, Lq, capacity, D, sms, requested)
+    return splits, attn_splitkv_kv8_workspace(B, Hq, Lq, capacity, D, splits, weights)
+
+
+def attn_splitkv_decode_kv8(q, cache: KV8Cache, scale: Optional[float] = None, kv_len=None, causal: bool = False,
+                            weights=None, num_splits: int = 0, out=None, lse=None, return_lse: bool = True,
+                            workspace=None, stream=None):
+    """attn_splitkv_decode over the 8-bit cache: q [B,Hq,Lq,D] (bf16 or fp16),
+    kv_len optional int32 device tensor [B] (default: the capacity).  causal:
+    query row i of Lq sees the first kv_len - Lq + 1 + i keys.
+    weights: optional float32 [B,Hkv,capacity]; each visible key's attention
+    weight, summed over the query rows of its kv head, is added to it (for
+    kv8_evict).  Returns (out, lse)."""
+    torch = _torch()
+    B, Hkv, capacity, D, block, code = _kv8(cache, q)
+    _consistent(q, {"kv_len": kv_len, "weights": weights, "out": out, "lse": lse}, same_dtype=("out",),
+                fp32=("weights", "lse"), int32=("kv_len",))
+    _expect(q.dim() == 4, "decode q is [B, Hq, Lq, D]")
+    _, Hq, Lq, _ = q.shape
+    _shape(q, (B, Hq, Lq, D), "q")
+    _shape(out, q.shape, "out")
+    _shape(lse, (B, Hq, Lq), "lse")
+    _shape(kv_len, (B,), "kv_len")
+    _shape(weights, (B, Hkv, capacity), "weights")
+    _need_cuda(q, kv_len, weights, out, lse)
+    if scale is None:
+        scale = D ** -0.5
+    if out is None:
+        out = torch.empty_like(q)
+    if return_lse and lse is None:
+        lse = torch.empty((B, Hq, Lq), dtype=torch.float32, device=q.device)
+    if not return_lse:
+        lse = None
+    splits, nbytes = _kv8_plan(B, Hq, Hkv, Lq, capacity, D, int(num_splits), weights is not None, q.device)
+    workspace, wbytes = _workspace(nbytes, q.device, workspace)
+    with _on(q.device):
+        st = lib().attn_splitkv_decode_kv8(
+            _ptr(q), _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scale), _ptr(cache.v_scale), _ptr(out), _ptr(lse),
+            _ptr(weights), B, Hq, Hkv, Lq, capacity, D, block, float(scale), _dtype_code(q), code, _ptr(kv_len),
+            int(bool(causal)), splits, _ptr(workspace), wbytes, _stream(stream, q.device))
+    _check(st, "attn_splitkv_decode_kv8")
+    return out, lse
+
+
+def kv8_evict(cache: KV8Cache, to: KV8Cache, weights, to_weights, kv_len, budget: int, sink: int = 0, recent: int = 0,
+              kept=None, new_len=None, stream=None):
+    """Cuts each sequence to `budget` tokens: its first `sink`, its last `recent`
+    and the heaviest of the rest by `weights` [B,Hkv,capacity] (float32, chosen
+    per head; equal weights: the lowest position), moved in order into `to` (a
+    cache that shares no memory with this one) with their weights into
+    `to_weights`.  kv_len: int32 device tensor [B] or None (the capacity).
+    Returns (kept int32 [B,Hkv,budget], -1 behind the last; new_len int32 [B])."""
+    torch = _torch()
+    B, Hkv, capacity, D, block, code = _kv8(cache, cache.k)
+    B2, H2, to_capacity, D2, block2, code2 = _kv8(to, cache.k, "to")
+    _expect((B2, H2, D2, block2, code2) == (B, Hkv, D, block, code), "the two caches differ in more than their capacity")
+    _consistent(cache.k, {"weights": weights, "to_weights": to_weights, "kv_len": kv_len, "kept": kept,
+                          "new_len": new_len}, fp32=("weights", "to_weights"), int32=("kv_len", "kept", "new_len"))
+    _expect(1 <= budget <= to_capacity, f"budget {budget} does not fit the capacity {to_capacity}")
+    _expect(sink >= 0 and recent >= 0 and sink + recent <= budget, "sink + recent must not exceed the budget")
+    _shape(weights, (B, Hkv, capacity), "weights")
+    _shape(to_weights, (B, Hkv, to_capacity), "to_weights")
+    _shape(kv_len, (B,), "kv_len")
+    _shape(kept, (B, Hkv, budget), "kept")
+    _shape(new_len, (B,), "new_len")
+    _need_cuda(weights, to_weights, kv_len, kept, new_len)
+    if kept is None:
+        kept = torch.empty((B, Hkv, budget), dtype=torch.int32, device=cache.k.device)
+    if new_len is None:
+        new_len = torch.empty((B,), dtype=torch.int32, device=cache.k.device)
+    with _on(cache.k.device):
+        st = lib().kv8_evict(_ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scale), _ptr(cache.v_scale), _ptr(weights),
+                             _ptr(kv_len), _ptr(to.k), _ptr(to.v), _ptr(to.k_scale), _ptr(to.v_scale),
+                             _ptr(to_weights), _ptr(kept), _ptr(new_len), B, Hkv, capacity, to_capacity, D, block, code,
+                             int(budget), int(sink), int(recent), _stream(stream, cache.k.device))
+    _check(st, "kv8_evict")
+    return kept, new_len
+
+
 __all__ = ["attn_fwd_lse", "attn_fwd_lse_chunks", "attn_fwd_lse_chunks_workspace", "attn_fwd_lse_int8", "attn_splitkv_decode", "attn_splitkv_decode_static", "merge_state",
            "attn_splitkv_plan", "attn_splitkv_workspace", "attn_splitkv_workspace_init", "attn_fwd_lse_workspace",
            "attn_fwd_lse_int8_workspace", "attn_varlen_plan", "device_error", "launch_count", "lib", "SkvError",
+           "rope_inv_freq", "rope_apply", "KV8Cache", "kv8_cache", "kv8_append", "kv8_fetch", "attn_splitkv_kv8_plan",
+           "attn_splitkv_kv8_workspace", "attn_splitkv_decode_kv8", "kv8_evict",
            "status_string", "LIB_PATH", "SIGNATURES"]

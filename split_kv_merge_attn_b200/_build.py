@@ -16,9 +16,9 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libsplitkv.so")
 
-SOURCES = ["skv_kernels.cu", "skv_abi.cpp", "skv_noalloc.cu"]
+SOURCES = ["skv_kernels.cu", "skv_abi.cpp", "skv_noalloc.cu", "skv_cache.cu"]
 HEADERS = ["skv_device.cuh", "skv_internal.h", "merge_state.cuh", "decode.cuh", "prefill.cuh",
-           "smooth.cuh", "tcgen05.cuh", "quant.cuh"]
+           "smooth.cuh", "tcgen05.cuh", "quant.cuh", "rope.cuh", "kv8.cuh", "decode_kv8.cuh", "evict.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

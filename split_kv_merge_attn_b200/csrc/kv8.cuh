@@ -1,0 +1,231 @@
+// The 8-bit key/value cache: codes [B, Hkv, capacity, D] (int8 or e4m3), one
+// fp32 scale per (block of tokens, head); a value is code * scale.
+//
+// Append.  The block's new tokens have the largest magnitude a; with qmax = 127
+// (int8) or 448 (e4m3)
+//   s = max(a / qmax, s_old)      s_old: the scale of older tokens of the block
+//   code = rne(x * (1 / s))       older codes c -> rne((c * s_old) * (1 / s)) if s > s_old
+// in fp32: one IEEE quotient and one reciprocal per block, one product per
+// value.  A scale below 2^-126 (its reciprocal would overflow) is stored as 0
+// with codes 0.  A NaN or infinity makes its block's scale NaN or infinite
+// with codes 0, so every value of the block reads back as NaN; codes
+// themselves are always finite.
+//
+// Bound by bytes (16 bits in, 8 out).  One CTA takes 128 tokens of one
+// (batch entry, head) of K or of V, each of its 8 warps 16 of them, which it
+// holds in registers between the maximum and the codes: one read, one write.
+// Every block size (16, 32, 64, 128) is then a whole number of warps.
+#pragma once
+
+#include "skv_device.cuh"
+
+namespace skv {
+
+constexpr int kKv8Window = 128;   // tokens per append CTA
+constexpr float kKv8TinyScale = 1.17549435e-38f;  // 2^-126
+
+template <bool kE4M3>
+struct Kv8Code {
+  static constexpr float kMax = kE4M3 ? 448.f : 127.f;
+  // four values already multiplied by 1 / scale (|.| <= kMax up to rounding)
+  static __device__ __forceinline__ uint32_t encode4(float x0, float x1, float x2, float x3) {
+    if constexpr (kE4M3) {
+      uint16_t lo, hi;
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x1), "f"(x0));
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x3), "f"(x2));
+      return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+    } else {
+      // adding 1.5 * 2^23 rounds to a whole number (ties to even) in the low
+      // bits; the low byte is the two's complement code
+      const uint32_t a = __float_as_uint(__fadd_rn(x0, 12582912.f)), b = __float_as_uint(__fadd_rn(x1, 12582912.f));
+      const uint32_t c = __float_as_uint(__fadd_rn(x2, 12582912.f)), d = __float_as_uint(__fadd_rn(x3, 12582912.f));
+      return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+    }
+  }
+  static __device__ __forceinline__ void decode4(uint32_t w, float (&x)[4]) {
+    if constexpr (kE4M3) {
+      uint32_t h0, h1;
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h0) : "h"(static_cast<uint16_t>(w & 0xffff)));
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h1) : "h"(static_cast<uint16_t>(w >> 16)));
+      const float2 f0 = unpack2<__half>(h0), f1 = unpack2<__half>(h1);
+      x[0] = f0.x; x[1] = f0.y; x[2] = f1.x; x[3] = f1.y;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = static_cast<float>(static_cast<int8_t>(w >> (8 * e)));
+    }
+  }
+};
+
+// 1 / s for a block's codes; 0 where the codes are 0 (s == 0, or not finite)
+__device__ __forceinline__ float kv8_inverse(float s) {
+  return (s > 0.f && s < INFINITY) ? __frcp_rn(s) : 0.f;
+}
+
+struct Kv8AppendArgs {
+  const void* x[2];         // new k, v
+  uint8_t* codes[2];
+  float* scale[2];          // [B, Hkv, capacity / block]
+  const int32_t* start;     // [B]
+  const int32_t* num_new;   // [B] or null (= S)
+  const int32_t* cu;        // [B + 1] (packed rows) or null
+  int B, Hkv, S, T, capacity, block;
+  int token_major;          // 1: rows ordered (b, s, h); 0: (b, h, s)
+};
+
+template <int D, typename T, bool kE4M3>
+__global__ void __launch_bounds__(256) kv8_append_kernel(const Kv8AppendArgs a) {
+  using Code = Kv8Code<kE4M3>;
+  constexpr int kLanes = D / 8;            // lanes of one row, 8 values each
+  constexpr int kRows = 32 / kLanes;       // rows a warp takes at once
+  constexpr int kPasses = 16 / kRows;
+  // a programmatic dependent of the kernel before it: waits before any load
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int b = blockIdx.y / a.Hkv, h = blockIdx.y % a.Hkv, which = blockIdx.z;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int start = min(max(a.start[b], 0), a.capacity);
+  int count = a.S, first_row = 0;
+  if (a.cu != nullptr) {
+    first_row = min(max(a.cu[b], 0), a.T);
+    count = min(max(a.cu[b + 1], first_row), a.T) - first_row;
+    count = min(count, a.S);
+  } else if (a.num_new != nullptr) {
+    count = min(max(a.num_new[b], 0), a.S);
+  }
+  const int end = start + min(count, a.capacity - start);
+  const int base = (start / kKv8Window + static_cast<int>(blockIdx.x)) * kKv8Window;
+  if (base >= end || start >= end) return;  // the whole CTA: nothing new in this window
+
+  const int cl = lane % kLanes, rl = lane / kLanes;
+  const int pos0 = base + warp * 16 + rl;   // this lane's rows: pos0 + kRows * p
+  const T* x = static_cast<const T*>(a.x[which]);
+  uint4 v[kPasses];
+  uint32_t top = 0;  // largest magnitude bits, two 16-bit halves
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) {
+    const int pos = pos0 + kRows * p;
+    v[p] = make_uint4(0, 0, 0, 0);
+    if (pos >= start && pos < end) {
+      int64_t row;
+      const int i = pos - start;
+      if (a.cu != nullptr) row = (static_cast<int64_t>(first_row) + i) * a.Hkv + h;
+      else if (a.token_major) row = (static_cast<int64_t>(b) * a.S + i) * a.Hkv + h;
+      else row = (static_cast<int64_t>(b) * a.Hkv + h) * a.S + i;
+      v[p] = __ldg(reinterpret_cast<const uint4*>(x + row * D + cl * 8));
+    }
+  }
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) {
+    // magnitude bits of 16-bit floats order as whole numbers, NaN above infinity
+    top = __vmaxu2(top, __vmaxu2(__vmaxu2(v[p].x & 0x7fff7fffu, v[p].y & 0x7fff7fffu),
+                                 __vmaxu2(v[p].z & 0x7fff7fffu, v[p].w & 0x7fff7fffu)));
+  }
+  top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+
+  __shared__ uint32_t warp_top[8];
+  const int per = a.block >> 4;            // warps of one block
+  const int group = warp / per;
+  const int block_pos = base + group * a.block;
+  const bool touched = block_pos < end && block_pos + a.block > start;
+  const int64_t at = (static_cast<int64_t>(b) * a.Hkv + h) * (a.capacity / a.block) + block_pos / a.block;
+  // a block that begins before `start` holds older tokens with a scale of their own
+  float s_old = 0.f;
+  if (touched && block_pos < start) s_old = a.scale[which][at];
+  if (lane == 0) warp_top[warp] = top;
+  __syncthreads();  // also orders every read of the old scale before its new value is written
+  if (!touched) return;
+  for (int w = group * per; w < (group + 1) * per; ++w) top = max(top, warp_top[w]);
+  const float amax = unpack2<T>(top).x;
+  const float fresh = __fdiv_rn(amax, Code::kMax);
+  float s = (fresh > s_old || isnan(fresh)) ? fresh : s_old;
+  if (s < kKv8TinyScale) s = 0.f;
+  const bool poisoned = !(s < INFINITY);
+  const float inv = kv8_inverse(s);
+  if (warp == group * per && lane == 0) a.scale[which][at] = s;
+
+  uint8_t* codes = a.codes[which] + (static_cast<int64_t>(b) * a.Hkv + h) * a.capacity * static_cast<int64_t>(D) + cl * 8;
+  const bool wider = s > s_old || (poisoned && s_old < INFINITY);
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) {
+    const int pos = pos0 + kRows * p;
+    if (pos >= end) continue;
+    uint2* dst = reinterpret_cast<uint2*>(codes + static_cast<int64_t>(pos) * D);
+    uint2 w = make_uint2(0, 0);
+    if (pos >= start) {
+      if (!poisoned) {
+        const float2 f0 = unpack2<T>(v[p].x), f1 = unpack2<T>(v[p].y), f2 = unpack2<T>(v[p].z), f3 = unpack2<T>(v[p].w);
+        w.x = Code::encode4(__fmul_rn(f0.x, inv), __fmul_rn(f0.y, inv), __fmul_rn(f1.x, inv), __fmul_rn(f1.y, inv));
+        w.y = Code::encode4(__fmul_rn(f2.x, inv), __fmul_rn(f2.y, inv), __fmul_rn(f3.x, inv), __fmul_rn(f3.y, inv));
+      }
+    } else {
+      if (!wider) continue;
+      if (!poisoned) {
+        w = *dst;
+        float c[4];
+        Code::decode4(w.x, c);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c[e] = __fmul_rn(__fmul_rn(c[e], s_old), inv);
+        w.x = Code::encode4(c[0], c[1], c[2], c[3]);
+        Code::decode4(w.y, c);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c[e] = __fmul_rn(__fmul_rn(c[e], s_old), inv);
+        w.y = Code::encode4(c[0], c[1], c[2], c[3]);
+      }
+    }
+    *dst = w;
+  }
+}
+
+// Fetch.  A window of the cache in 16 bits: out[b, h, i] = code * scale of
+// position start[b] + i, zero where that is not in [0, kv_len[b]).  Bound by
+// bytes (8 bits in, 16 out): one thread per 16 codes of K and of V.
+struct Kv8FetchArgs {
+  const uint8_t* codes[2];
+  const float* scale[2];
+  void* out[2];
+  const int32_t* start;    // [B] or null (= 0)
+  const int32_t* kv_len;   // [B] or null (= capacity)
+  int B, Hkv, capacity, block, n, D;
+  int token_major;         // out [B, n, Hkv, D] instead of [B, Hkv, n, D]
+};
+
+template <typename T, bool kE4M3>
+__global__ void __launch_bounds__(256) kv8_fetch_kernel(const Kv8FetchArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int units = a.D >> 4;
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  const int64_t row = id / units;             // (b, h, i)
+  const int u = static_cast<int>(id - row * units);
+  if (row >= static_cast<int64_t>(a.B) * a.Hkv * a.n) return;
+  const int64_t bh = row / a.n;
+  const int i = static_cast<int>(row - bh * a.n);
+  const int b = static_cast<int>(bh / a.Hkv), h = static_cast<int>(bh - static_cast<int64_t>(b) * a.Hkv);
+  const int64_t pos = static_cast<int64_t>(a.start != nullptr ? a.start[b] : 0) + i;
+  const int len = a.kv_len != nullptr ? min(a.kv_len[b], a.capacity) : a.capacity;
+  const int which = blockIdx.y;
+  uint4 o0 = make_uint4(0, 0, 0, 0), o1 = o0;
+  if (pos >= 0 && pos < len) {
+    const float s = a.scale[which][bh * (a.capacity / a.block) + pos / a.block];
+    const uint4 w = *reinterpret_cast<const uint4*>(a.codes[which] + (bh * a.capacity + pos) * a.D + u * 16);
+    float x[4];
+    Kv8Code<kE4M3>::decode4(w.x, x);
+    o0.x = pack2<T>(x[0] * s, x[1] * s);
+    o0.y = pack2<T>(x[2] * s, x[3] * s);
+    Kv8Code<kE4M3>::decode4(w.y, x);
+    o0.z = pack2<T>(x[0] * s, x[1] * s);
+    o0.w = pack2<T>(x[2] * s, x[3] * s);
+    Kv8Code<kE4M3>::decode4(w.z, x);
+    o1.x = pack2<T>(x[0] * s, x[1] * s);
+    o1.y = pack2<T>(x[2] * s, x[3] * s);
+    Kv8Code<kE4M3>::decode4(w.w, x);
+    o1.z = pack2<T>(x[0] * s, x[1] * s);
+    o1.w = pack2<T>(x[2] * s, x[3] * s);
+  }
+  const int64_t orow = a.token_major ? (static_cast<int64_t>(b) * a.n + i) * a.Hkv + h : row;
+  uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out[which]) + orow * a.D + u * 16);
+  dst[0] = o0;
+  dst[1] = o1;
+}
+
+}  // namespace skv

@@ -112,7 +112,12 @@ uint64_t skv_launch_count(void) { return skv::launch_count(); }
 
 skv_status skv_device_error(int* code) {
   if (code == nullptr) return SKV_ERR_INVALID_ARG;
-  return cuda_status(skv::read_and_clear_device_error(code));
+  int first = 0, second = 0;
+  int e = skv::read_and_clear_device_error(&first);
+  if (e == 0) e = skv::read_and_clear_cache_error(&second);
+  if (e != 0) return cuda_status(e);
+  *code = first != 0 ? first : second;
+  return SKV_OK;
 }
 
 // ------------------------------------------------------------------ planning

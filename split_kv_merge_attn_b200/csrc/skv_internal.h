@@ -17,6 +17,8 @@ enum DeviceError : int {
   kErrDecodeFullWait = 0x102,
   kErrDecodeCounter = 0x103,   // a decode arrival counter was not zero before the call
   kErrPrefillWait = 0x201,
+  kErrKv8EmptyWait = 0x301,
+  kErrKv8FullWait = 0x302,
 };
 
 // Constants of the split planner (mirrored by the decode kernel).
@@ -113,6 +115,9 @@ int launch_smooth_k(const void* k, void* k_smoothed, float* kmean, float* partia
                     int kv_ranges = 1, const int32_t* kv_bounds = nullptr);
 
 int read_and_clear_device_error(int* code);
+// The same for the error word of the 8-bit cache's kernels (a translation unit
+// of their own, and so a word of their own).
+int read_and_clear_cache_error(int* code);
 
 // Elementwise evaluation of the prefill's FMA-pipe exp2 (diagnostics).
 int launch_exp2_fma(const float* x, float* y, int64_t n, skv_stream_t stream);

@@ -1,0 +1,98 @@
+"""The operators together, as a serving loop uses them: rotary positions, a
+prompt appended to the 8-bit cache, decode steps that gather weights, eviction,
+and decoding on; then attention over the cached prefix through attn_fwd_lse."""
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+import split_kv_merge_attn_b200 as skv
+from tests._gpu_helpers import check_lse, check_o, vmax
+from tests._kv8_helpers import gen, i32, values
+from tests.test_gpu_kv8_decode import check
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("codes", ["int8", "e4m3"])
+def test_serving_loop(codes):
+    B, Hq, Hkv, D, block, capacity, budget = 2, 8, 2, 128, 32, 512, 128
+    g = gen(1)
+    prompt = [200, 77]
+    S = max(prompt)
+    inv_freq, factor = skv.rope_inv_freq(64, scaling="yarn", factor=4.0, original_len=128)
+    cache = skv.kv8_cache(B, Hkv, capacity, D, block, codes)
+    small = skv.kv8_cache(B, Hkv, budget, D, block, codes)
+    weights, small_w = torch.zeros(B, Hkv, capacity, device="cuda"), torch.zeros(B, Hkv, budget, device="cuda")
+    length = i32([0, 0])
+
+    # ---- the prompt, token-major as projections leave it
+    q, k, v = (torch.randn(B, S, H, D, generator=g).bfloat16().cuda() for H in (Hq, Hkv, Hkv))
+    pos = torch.arange(S, dtype=torch.int32, device="cuda").expand(B, S).contiguous()
+    q, k = skv.rope_apply(q, k, pos, inv_freq, layout="NHD", factor=factor, q_out=q, k_out=k)
+    skv.kv8_append(cache, k, v, length, num_new=i32(prompt), layout="NHD")
+    length += i32(prompt)
+    # the cache holds the keys to half a code step of their block's scale (e4m3:
+    # 2^-4 of the value, or half of 2^-9 scales).  The scaled value that is rounded
+    # to a code carries three fp32 roundings (s, 1 / s, the product): of at most
+    # 127 codes, 127 * 3 * 2^-24 < 2^-15 codes, i.e. 2^-14 of the half step.
+    for b in range(B):
+        n = prompt[b]
+        held = values(cache.k, cache.k_scale, prompt)[b, :, :n]
+        want = O.to_f64(k)[b, :n].transpose(1, 0, 2)
+        s = np.repeat(cache.k_scale[b].cpu().double().numpy(), block, -1)[:, :n, None]
+        step = 0.5 * s if codes == "int8" else np.maximum(2.0 ** -4 * np.abs(want), 2.0 ** -10 * s)
+        assert np.all(np.abs(held - want) <= step * (1 + 2.0 ** -14))
+
+    # ---- decode steps
+    def step(cache, weights, length, at):
+        q, k, v = (torch.randn(B, H, 1, D, generator=g).bfloat16().cuda() for H in (Hq, Hkv, Hkv))
+        q, k = skv.rope_apply(q, k, at.view(B, 1), inv_freq, factor=factor)
+        skv.kv8_append(cache, k, v, length)
+        length += 1
+        before = weights.clone()
+        out, lse = skv.attn_splitkv_decode_kv8(q, cache, kv_len=length, weights=weights)
+        n = length.tolist()
+        check(q, cache, out, lse, n, D ** -0.5, False, "bf16")
+        for b in range(B):  # what this step added is each key's weight
+            added = (weights - before)[b, :, : n[b]].double().sum(-1).cpu().numpy()
+            assert np.all(np.abs(added - Hq // Hkv) <= 2.0 ** -14)
+            assert torch.equal(weights[b, :, n[b]:], before[b, :, n[b]:])
+        return out
+
+    position = i32(prompt)
+    for _ in range(5):
+        step(cache, weights, length, position)
+        position = position + 1
+
+    # ---- eviction: 4 sinks, the last 32, the heaviest between; one sequence is short enough to stay
+    n = length.tolist()
+    kept, length = skv.kv8_evict(cache, small, weights, small_w, length, budget - 32, sink=4, recent=32)
+    assert length.tolist() == [min(x, budget - 32) for x in n]
+    for b in range(B):
+        for h in range(Hkv):
+            at = O.kv8_kept(weights[b, h].cpu(), n[b], budget - 32, 4, 32)
+            assert kept[b, h, : len(at)].tolist() == at.tolist()
+    # decoding goes on at the old positions over the smaller cache
+    for _ in range(5):
+        step(small, small_w, length, position)
+        position = position + 1
+    torch.cuda.synchronize()
+    assert skv.device_error() == 0
+
+
+def test_prefill_over_a_cached_prefix():
+    """A prefix read back from the cache in 16 bits joins new keys by merge_state."""
+    B, Hq, Hkv, D, n, S = 1, 4, 2, 128, 300, 96
+    g = gen(2)
+    cache = skv.kv8_cache(B, Hkv, 384, D, 64, "int8")
+    k0, v0 = (torch.randn(B, Hkv, n, D, generator=g).bfloat16().cuda() for _ in range(2))
+    skv.kv8_append(cache, k0, v0, i32([0]))
+    q = torch.randn(B, Hq, S, D, generator=g).bfloat16().cuda()
+    k1, v1 = (torch.randn(B, Hkv, S, D, generator=g).bfloat16().cuda() for _ in range(2))
+    k, v = skv.kv8_fetch(cache, n, torch.bfloat16, kv_len=i32([n]))
+    parts = [skv.attn_fwd_lse(q, k, v), skv.attn_fwd_lse(q, k1, v1, causal=True)]
+    out, lse = skv.merge_state(torch.stack([p[0] for p in parts]), torch.stack([p[1] for p in parts]))
+    o_ref, l_ref = O.dense(q, torch.cat((k, k1), 2), torch.cat((v, v1), 2), D ** -0.5, causal=True)
+    check_o(out, o_ref, vmax(torch.cat((v, v1), 2)))
+    check_lse(lse, l_ref)
