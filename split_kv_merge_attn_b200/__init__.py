@@ -192,23 +192,63 @@ def _workspace(nbytes: int, device, workspace):
     return workspace, workspace.numel() * workspace.element_size()
 
 
-class _Here:
-    """A context that leaves the current device as it is."""
+class _Runtime:
+    """What the short-call wrappers need of PyTorch, looked up once."""
 
-    def __enter__(self):
-        return self
+    def __init__(self):
+        torch = _torch()
+        self.torch = torch
+        self.int32, self.float32, self.float64 = torch.int32, torch.float32, torch.float64
+        self.half = {torch.bfloat16: 0, torch.float16: 1}
+        self.codes = {torch.int8: 0, torch.float8_e4m3fn: 1}
+        self.empty, self.empty_like = torch.empty, torch.empty_like
+        self.current_device = torch.cuda.current_device
+        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
-    def __exit__(self, *exc):
-        return False
+
+@functools.lru_cache(maxsize=None)
+def _runtime() -> _Runtime:
+    return _Runtime()
 
 
-_HERE = _Here()
+def _refuse(name, t, shape, dtype, dev) -> None:
+    """Says what is wrong with a tensor that _arg did not take."""
+    _expect(t is not None, f"{name} is needed")
+    _expect(t.dtype == dtype, f"{name} has dtype {t.dtype}, expected {dtype}")
+    _expect(tuple(t.shape) == tuple(shape), f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    _need_cuda(t)
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
 
 
-def _on(device):
-    """Makes the tensors' device current for a call (launches go to the current device)."""
-    torch = _torch()
-    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+def _arg(name, t, shape, dtype, dev) -> int:
+    """The address of a tensor of exactly this shape, type and device, contiguous."""
+    if t is None or t.dtype != dtype or t.shape != shape or t.get_device() != dev or dev < 0 or not t.is_contiguous():
+        _refuse(name, t, shape, dtype, dev)
+    return t.data_ptr()
+
+
+def _opt(name, t, shape, dtype, dev) -> Optional[int]:
+    return None if t is None else _arg(name, t, shape, dtype, dev)
+
+
+def _half(rt, dtype, name: str) -> int:
+    code = rt.half.get(dtype)
+    _expect(code is not None, f"{name} must be bfloat16 or float16" if code is None else "")
+    return code
+
+
+def _call(rt, what: str, dev: int, stream, *args) -> None:
+    """Calls the library with `dev` current and the stream as the last argument."""
+    fn = getattr(lib(), what)
+    s = rt.raw_stream(dev) if stream is None else stream.cuda_stream
+    if rt.current_device() == dev:
+        st = fn(*args, s)
+    else:
+        with rt.torch.cuda.device(dev):
+            st = fn(*args, s)
+    if st != SKV_OK:
+        raise SkvError(st, what)
 
 
 # ------------------------------------------------------------------ queries
@@ -590,41 +630,36 @@ def rope_apply(q, k, positions, inv_freq, layout: str = "HND", interleaved: bool
     (2i, 2i+1) instead of (i, i + R/2).  inverse: the transpose, i.e. the
     gradient of the inputs given that of the outputs.  q_out=q, k_out=k work in
     place.  Returns (q_out, k_out)."""
-    torch = _torch()
-    _expect(layout in LAYOUTS, f"unknown layout {layout!r}")
-    _expect(q.dim() == (3 if layout == "TND" else 4), f"{layout} q has {q.dim()} dimensions")
-    _consistent(q, {"k": k, "positions": positions, "inv_freq": inv_freq, "q_out": q_out, "k_out": k_out},
-                same_dtype=("k", "q_out", "k_out"), int32=("positions",))
-    _expect(inv_freq.dtype == torch.float64, f"inv_freq must be float64, got {inv_freq.dtype}")
-    _expect(inv_freq.dim() == 1, "inv_freq is [rotary_dim / 2]")
+    rt = _runtime()
+    if layout not in LAYOUTS or q.dim() != (3 if layout == "TND" else 4):
+        raise ValueError(f"unknown layout {layout!r}, or q has not its dimensions ({q.dim()})")
+    shape, dt, dev = q.shape, q.dtype, q.get_device()
     if layout == "HND":
-        B, Hq, S, D = q.shape
+        B, Hq, S, D = shape
     elif layout == "NHD":
-        B, S, Hq, D = q.shape
+        B, S, Hq, D = shape
     else:
-        B, (S, Hq, D) = 1, q.shape
-    Hkv = 0
+        B, (S, Hq, D) = 1, shape
+    code = _half(rt, dt, "q")
+    pq = _arg("q", q, shape, dt, dev)
+    pk, Hkv = None, 0
     if k is not None:
-        _expect(k.dim() == q.dim(), f"{layout} k has {k.dim()} dimensions")
-        Hkv = k.shape[1 if layout != "NHD" else 2]
-        _shape(k, {"HND": (B, Hkv, S, D), "NHD": (B, S, Hkv, D), "TND": (S, Hkv, D)}[layout], "k")
-    _shape(positions, (S,) if layout == "TND" else (B, S), "positions")
-    _shape(q_out, q.shape, "q_out")
-    _expect(k is not None or k_out is None, "k_out without k")
-    if k is not None:
-        _shape(k_out, k.shape, "k_out")
-    _need_cuda(q, k, positions, inv_freq, q_out, k_out)
+        Hkv = k.shape[2 if layout == "NHD" else 1] if k.dim() == q.dim() else 0
+        k_shape = (B, Hkv, S, D) if layout == "HND" else ((B, S, Hkv, D) if layout == "NHD" else (S, Hkv, D))
+        pk = _arg("k", k, k_shape, dt, dev)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    pp = _arg("positions", positions, (S,) if layout == "TND" else (B, S), rt.int32, dev)
+    pf = _arg("inv_freq", inv_freq, (inv_freq.numel(),), rt.float64, dev)
     if q_out is None:
-        q_out = torch.empty_like(q)
+        q_out = rt.empty_like(q)
     if k_out is None and k is not None:
-        k_out = torch.empty_like(k)
-    if S == 0:
-        return q_out, k_out
-    with _on(q.device):
-        st = lib().rope_apply(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), _ptr(positions), _ptr(inv_freq), B, Hq, Hkv,
-                              S, D, 2 * inv_freq.numel(), float(factor), _dtype_code(q), LAYOUTS[layout],
-                              int(bool(interleaved)), int(bool(inverse)), _stream(stream, q.device))
-    _check(st, "rope_apply")
+        k_out = rt.empty_like(k)
+    pqo = _arg("q_out", q_out, shape, dt, dev)
+    pko = None if k is None else _arg("k_out", k_out, k_shape, dt, dev)
+    if S and B:
+        _call(rt, "rope_apply", dev, stream, pq, pk, pqo, pko, pp, pf, B, Hq, Hkv, S, D, 2 * inv_freq.numel(),
+              float(factor), code, LAYOUTS[layout], 1 if interleaved else 0, 1 if inverse else 0)
     return q_out, k_out
 
 
@@ -652,22 +687,18 @@ def kv8_cache(B: int, Hkv: int, capacity: int, D: int, block: int = 64, codes: s
     return KV8Cache(*code, *scale)
 
 
-def _kv8(cache, ref, what: str = "cache"):
-    """Checks a cache's tensors (on the device of `ref`): (B, Hkv, capacity, D, block, code)."""
-    torch = _torch()
+def _kv8(rt, cache, dev, what: str = "cache"):
+    """Checks a cache's tensors on device `dev`: (its four addresses, B, Hkv,
+    capacity, D, block, code)."""
     k, v, ks, vs = cache
-    _expect(k.dim() == 4, f"{what}.k is [B, Hkv, capacity, D]")
-    _expect(k.dtype in (torch.int8, torch.float8_e4m3fn), f"{what}.k has dtype {k.dtype}")
-    _expect(v.dtype == k.dtype and v.shape == k.shape, f"{what}.v must be like {what}.k")
-    _expect(ks.dtype == torch.float32 and vs.dtype == torch.float32, f"{what} scales must be float32")
-    B, Hkv, capacity, D = k.shape
-    blocks = ks.shape[-1] if ks.dim() == 3 else 0
-    _expect(blocks > 0 and capacity % blocks == 0 and ks.shape == (B, Hkv, blocks) and vs.shape == ks.shape,
-            f"{what} scales are [B, Hkv, capacity / block]")
-    for t in cache:
-        _expect(t.device == ref.device, f"{what} is on {t.device}, expected {ref.device}")
-    _need_cuda(k, v, ks, vs)
-    return B, Hkv, capacity, D, capacity // blocks, 0 if k.dtype == torch.int8 else 1
+    shape, code = k.shape, rt.codes.get(k.dtype)
+    if code is None or len(shape) != 4 or ks.dim() != 3 or ks.shape[2] == 0 or shape[2] % ks.shape[2]:
+        raise ValueError(f"{what}: codes are int8 or float8_e4m3fn [B, Hkv, capacity, D], scales [B, Hkv, capacity / block]")
+    B, Hkv, capacity, D = shape
+    blocks = (B, Hkv, ks.shape[2])
+    at = (_arg(what + ".k", k, shape, k.dtype, dev), _arg(what + ".v", v, shape, k.dtype, dev),
+          _arg(what + ".k_scale", ks, blocks, rt.float32, dev), _arg(what + ".v_scale", vs, blocks, rt.float32, dev))
+    return at, B, Hkv, capacity, D, capacity // blocks[2], code
 
 
 def kv8_append(cache: KV8Cache, k, v, start, num_new=None, layout: str = "HND", cu_seqlens=None,
@@ -680,35 +711,27 @@ def kv8_append(cache: KV8Cache, k, v, start, num_new=None, layout: str = "HND", 
     first num_new[b] tokens only (dense layouts).  Positions and counts are
     clamped on the device; tokens behind the capacity are dropped.  A block's
     scale grows with its largest value and its older codes follow."""
-    B, Hkv, capacity, D, block, code = _kv8(cache, k)
-    _expect(layout in LAYOUTS, f"unknown layout {layout!r}")
-    _consistent(k, {"v": v, "start": start, "num_new": num_new, "cu_seqlens": cu_seqlens}, same_dtype=("v",),
-                int32=("start", "num_new", "cu_seqlens"))
+    rt = _runtime()
+    dt, dev = k.dtype, k.get_device()
+    at, B, Hkv, capacity, D, block, code = _kv8(rt, cache, dev)
     T = 0
     if layout == "TND":
-        _expect(cu_seqlens is not None and max_seqlen is not None, "TND layout needs cu_seqlens and max_seqlen")
-        _expect(num_new is None, "TND lengths are those of cu_seqlens")
-        _expect(k.dim() == 3, "TND tensors are [tokens, heads, D]")
+        if cu_seqlens is None or max_seqlen is None or num_new is not None or k.dim() != 3:
+            raise ValueError("TND rows are [tokens, heads, D], with cu_seqlens and max_seqlen and without num_new")
         T, S = k.shape[0], int(max_seqlen)
-        _shape(k, (T, Hkv, D), "k")
-        _shape(cu_seqlens, (B + 1,), "cu_seqlens")
+        shape = (T, Hkv, D)
     else:
-        _expect(cu_seqlens is None and max_seqlen is None, "cu_seqlens and max_seqlen belong to the TND layout")
-        _expect(k.dim() == 4, f"{layout} tensors are 4-D")
+        if layout not in LAYOUTS or cu_seqlens is not None or max_seqlen is not None or k.dim() != 4:
+            raise ValueError(f"layout {layout!r}: rows are 4-D, without cu_seqlens and max_seqlen")
         S = k.shape[2 if layout == "HND" else 1]
-        _shape(k, (B, Hkv, S, D) if layout == "HND" else (B, S, Hkv, D), "k")
-    _shape(v, k.shape, "v")
-    _expect(start is not None, "start is needed")
-    _shape(start, (B,), "start")
-    _shape(num_new, (B,), "num_new")
-    _need_cuda(k, v, start, num_new, cu_seqlens)
-    if k.numel() == 0:
-        return cache
-    with _on(k.device):
-        st = lib().kv8_append(_ptr(k), _ptr(v), _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scale), _ptr(cache.v_scale),
-                              _ptr(start), _ptr(num_new), _ptr(cu_seqlens), B, Hkv, S, T, capacity, D, block,
-                              _dtype_code(k), code, LAYOUTS[layout], _stream(stream, k.device))
-    _check(st, "kv8_append")
+        shape = (B, Hkv, S, D) if layout == "HND" else (B, S, Hkv, D)
+    pk, pv = _arg("k", k, shape, dt, dev), _arg("v", v, shape, dt, dev)
+    ps = _arg("start", start, (B,), rt.int32, dev)
+    pn, pc = _opt("num_new", num_new, (B,), rt.int32, dev), _opt("cu_seqlens", cu_seqlens, (B + 1,), rt.int32, dev)
+    half = _half(rt, dt, "k")
+    if S and (T or layout != "TND"):
+        _call(rt, "kv8_append", dev, stream, pk, pv, *at, ps, pn, pc, B, Hkv, S, T, capacity, D, block, half, code,
+              LAYOUTS[layout])
     return cache
 
 
@@ -717,31 +740,24 @@ def kv8_fetch(cache: KV8Cache, n: int, dtype=None, start=None, kv_len=None, layo
     """A window of n tokens of every sequence in 16 bits: (k, v) [B,Hkv,n,D] (HND)
     or [B,n,Hkv,D] (NHD), token i from position start[b] + i (start: int32 device
     tensor [B], default 0); zero at positions outside [0, kv_len[b])."""
-    torch = _torch()
-    B, Hkv, capacity, D, block, code = _kv8(cache, cache.k)
-    _expect(layout in ("HND", "NHD"), f"kv8_fetch takes HND or NHD, not {layout}")
-    _expect(n >= 0, "n must not be negative")
-    _consistent(cache.k, {"start": start, "kv_len": kv_len, "k_out": k_out, "v_out": v_out}, int32=("start", "kv_len"))
-    if dtype is None:
-        dtype = k_out.dtype if k_out is not None else torch.bfloat16
+    rt = _runtime()
+    dev = cache.k.get_device()
+    at, B, Hkv, capacity, D, block, code = _kv8(rt, cache, dev)
+    if layout not in ("HND", "NHD") or n < 0:
+        raise ValueError(f"kv8_fetch takes HND or NHD, not {layout!r}, and n >= 0, not {n}")
     shape = (B, Hkv, n, D) if layout == "HND" else (B, n, Hkv, D)
-    for name, t in (("k_out", k_out), ("v_out", v_out)):
-        _shape(t, shape, name)
-        _expect(t is None or t.dtype == dtype, f"{name} must be {dtype}")
-    _shape(start, (B,), "start")
-    _shape(kv_len, (B,), "kv_len")
-    _need_cuda(start, kv_len, k_out, v_out)
+    if dtype is None:
+        dtype = k_out.dtype if k_out is not None else rt.torch.bfloat16
+    half = _half(rt, dtype, "dtype")
+    ps, pl = _opt("start", start, (B,), rt.int32, dev), _opt("kv_len", kv_len, (B,), rt.int32, dev)
     if k_out is None:
-        k_out = torch.empty(shape, dtype=dtype, device=cache.k.device)
+        k_out = rt.empty(shape, dtype=dtype, device=cache.k.device)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=dtype, device=cache.k.device)
-    if n == 0:
-        return k_out, v_out
-    with _on(cache.k.device):
-        st = lib().kv8_fetch(_ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scale), _ptr(cache.v_scale), _ptr(k_out),
-                             _ptr(v_out), _ptr(start), _ptr(kv_len), B, Hkv, int(n), capacity, D, block,
-                             _dtype_code(k_out), code, LAYOUTS[layout], _stream(stream, cache.k.device))
-    _check(st, "kv8_fetch")
+        v_out = rt.empty_like(k_out)
+    pk, pv = _arg("k_out", k_out, shape, dtype, dev), _arg("v_out", v_out, shape, dtype, dev)
+    if n:
+        _call(rt, "kv8_fetch", dev, stream, *at, pk, pv, ps, pl, B, Hkv, int(n), capacity, D, block, half, code,
+              LAYOUTS[layout])
     return k_out, v_out
 
 
@@ -762,7 +778,7 @@ def attn_splitkv_kv8_workspace(B: int, Hq: int, Lq: int, capacity: int, D: int, 
 @functools.lru_cache(maxsize=256)
 def _kv8_plan(B, Hq, Hkv, Lq, capacity, D, requested, weights, device):
     """(splits, workspace bytes): a function of the sizes and the device's SM count."""
-    sms = _torch().cuda.get_device_properties(device).multi_processor_count
+    sms = _runtime().torch.cuda.get_device_properties(device).multi_processor_count
     splits = attn_splitkv_kv8_plan(B, Hq, Hkv, Lq, capacity, D, sms, requested)
     return splits, attn_splitkv_kv8_workspace(B, Hq, Lq, capacity, D, splits, weights)
 
@@ -776,34 +792,30 @@ def attn_splitkv_decode_kv8(q, cache: KV8Cache, scale: Optional[float] = None, k
     weights: optional float32 [B,Hkv,capacity]; each visible key's attention
     weight, summed over the query rows of its kv head, is added to it (for
     kv8_evict).  Returns (out, lse)."""
-    torch = _torch()
-    B, Hkv, capacity, D, block, code = _kv8(cache, q)
-    _consistent(q, {"kv_len": kv_len, "weights": weights, "out": out, "lse": lse}, same_dtype=("out",),
-                fp32=("weights", "lse"), int32=("kv_len",))
-    _expect(q.dim() == 4, "decode q is [B, Hq, Lq, D]")
-    _, Hq, Lq, _ = q.shape
-    _shape(q, (B, Hq, Lq, D), "q")
-    _shape(out, q.shape, "out")
-    _shape(lse, (B, Hq, Lq), "lse")
-    _shape(kv_len, (B,), "kv_len")
-    _shape(weights, (B, Hkv, capacity), "weights")
-    _need_cuda(q, kv_len, weights, out, lse)
-    if scale is None:
-        scale = D ** -0.5
+    rt = _runtime()
+    shape, dt, dev = q.shape, q.dtype, q.get_device()
+    at, B, Hkv, capacity, D, block, code = _kv8(rt, cache, dev)
+    if len(shape) != 4:
+        raise ValueError("decode q is [B, Hq, Lq, D]")
+    Hq, Lq = shape[1], shape[2]
+    pq, half = _arg("q", q, (B, Hq, Lq, D), dt, dev), _half(rt, dt, "q")
+    pn = _opt("kv_len", kv_len, (B,), rt.int32, dev)
+    pw = _opt("weights", weights, (B, Hkv, capacity), rt.float32, dev)
+    splits, need = _kv8_plan(B, Hq, Hkv, Lq, capacity, D, int(num_splits), pw is not None, dev)
     if out is None:
-        out = torch.empty_like(q)
-    if return_lse and lse is None:
-        lse = torch.empty((B, Hq, Lq), dtype=torch.float32, device=q.device)
+        out = rt.empty_like(q)
     if not return_lse:
         lse = None
-    splits, nbytes = _kv8_plan(B, Hq, Hkv, Lq, capacity, D, int(num_splits), weights is not None, q.device)
-    workspace, wbytes = _workspace(nbytes, q.device, workspace)
-    with _on(q.device):
-        st = lib().attn_splitkv_decode_kv8(
-            _ptr(q), _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scale), _ptr(cache.v_scale), _ptr(out), _ptr(lse),
-            _ptr(weights), B, Hq, Hkv, Lq, capacity, D, block, float(scale), _dtype_code(q), code, _ptr(kv_len),
-            int(bool(causal)), splits, _ptr(workspace), wbytes, _stream(stream, q.device))
-    _check(st, "attn_splitkv_decode_kv8")
+    elif lse is None:
+        lse = rt.empty((B, Hq, Lq), dtype=rt.float32, device=q.device)
+    if workspace is None and need:
+        workspace = rt.empty(need, dtype=rt.torch.uint8, device=q.device)
+    ws, wbytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    if workspace is not None and workspace.get_device() != dev:
+        raise ValueError(f"workspace is on {workspace.device}, q on {q.device}")
+    _call(rt, "attn_splitkv_decode_kv8", dev, stream, pq, *at, _arg("out", out, shape, dt, dev),
+          _opt("lse", lse, (B, Hq, Lq), rt.float32, dev), pw, B, Hq, Hkv, Lq, capacity, D, block,
+          float(D ** -0.5 if scale is None else scale), half, code, pn, 1 if causal else 0, splits, ws, wbytes)
     return out, lse
 
 
@@ -815,30 +827,24 @@ def kv8_evict(cache: KV8Cache, to: KV8Cache, weights, to_weights, kv_len, budget
     cache that shares no memory with this one) with their weights into
     `to_weights`.  kv_len: int32 device tensor [B] or None (the capacity).
     Returns (kept int32 [B,Hkv,budget], -1 behind the last; new_len int32 [B])."""
-    torch = _torch()
-    B, Hkv, capacity, D, block, code = _kv8(cache, cache.k)
-    B2, H2, to_capacity, D2, block2, code2 = _kv8(to, cache.k, "to")
-    _expect((B2, H2, D2, block2, code2) == (B, Hkv, D, block, code), "the two caches differ in more than their capacity")
-    _consistent(cache.k, {"weights": weights, "to_weights": to_weights, "kv_len": kv_len, "kept": kept,
-                          "new_len": new_len}, fp32=("weights", "to_weights"), int32=("kv_len", "kept", "new_len"))
-    _expect(1 <= budget <= to_capacity, f"budget {budget} does not fit the capacity {to_capacity}")
-    _expect(sink >= 0 and recent >= 0 and sink + recent <= budget, "sink + recent must not exceed the budget")
-    _shape(weights, (B, Hkv, capacity), "weights")
-    _shape(to_weights, (B, Hkv, to_capacity), "to_weights")
-    _shape(kv_len, (B,), "kv_len")
-    _shape(kept, (B, Hkv, budget), "kept")
-    _shape(new_len, (B,), "new_len")
-    _need_cuda(weights, to_weights, kv_len, kept, new_len)
+    rt = _runtime()
+    dev = cache.k.get_device()
+    at, B, Hkv, capacity, D, block, code = _kv8(rt, cache, dev)
+    to_at, B2, H2, to_capacity, D2, block2, code2 = _kv8(rt, to, dev, "to")
+    if (B2, H2, D2, block2, code2) != (B, Hkv, D, block, code):
+        raise ValueError("the two caches differ in more than their capacity")
+    if not (1 <= budget <= to_capacity and sink >= 0 and recent >= 0 and sink + recent <= budget):
+        raise ValueError(f"budget {budget} must fit the capacity {to_capacity} and hold sink {sink} + recent {recent}")
+    pw = _arg("weights", weights, (B, Hkv, capacity), rt.float32, dev)
+    pt = _arg("to_weights", to_weights, (B, Hkv, to_capacity), rt.float32, dev)
+    pl = _opt("kv_len", kv_len, (B,), rt.int32, dev)
     if kept is None:
-        kept = torch.empty((B, Hkv, budget), dtype=torch.int32, device=cache.k.device)
+        kept = rt.empty((B, Hkv, budget), dtype=rt.int32, device=weights.device)
     if new_len is None:
-        new_len = torch.empty((B,), dtype=torch.int32, device=cache.k.device)
-    with _on(cache.k.device):
-        st = lib().kv8_evict(_ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scale), _ptr(cache.v_scale), _ptr(weights),
-                             _ptr(kv_len), _ptr(to.k), _ptr(to.v), _ptr(to.k_scale), _ptr(to.v_scale),
-                             _ptr(to_weights), _ptr(kept), _ptr(new_len), B, Hkv, capacity, to_capacity, D, block, code,
-                             int(budget), int(sink), int(recent), _stream(stream, cache.k.device))
-    _check(st, "kv8_evict")
+        new_len = rt.empty((B,), dtype=rt.int32, device=weights.device)
+    _call(rt, "kv8_evict", dev, stream, *at, pw, pl, *to_at, pt, _arg("kept", kept, (B, Hkv, budget), rt.int32, dev),
+          _arg("new_len", new_len, (B,), rt.int32, dev), B, Hkv, capacity, to_capacity, D, block, code, int(budget),
+          int(sink), int(recent))
     return kept, new_len
 
 

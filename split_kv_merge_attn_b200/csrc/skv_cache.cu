@@ -128,7 +128,9 @@ int encode_codes(CUtensorMap* m, const void* base, int64_t tokens, int D) {
   const cuuint64_t width = D == 256 ? 256 : 128;
   const cuuint64_t dims[2] = {width, static_cast<cuuint64_t>(tokens) * D / width};
   const cuuint64_t strides[1] = {width};
-  const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(D == 64 ? kKv8Tile / 2 : kKv8Tile)};
+  const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(D == 64    ? Kv8DecodeCfg<64>::kBoxRows
+                                                          : D == 128 ? Kv8DecodeCfg<128>::kBoxRows
+                                                                     : Kv8DecodeCfg<256>::kBoxRows)};
   const cuuint32_t one[2] = {1, 1};
   const CUresult r = encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, one,
                             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,

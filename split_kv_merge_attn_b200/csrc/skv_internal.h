@@ -17,8 +17,7 @@ enum DeviceError : int {
   kErrDecodeFullWait = 0x102,
   kErrDecodeCounter = 0x103,   // a decode arrival counter was not zero before the call
   kErrPrefillWait = 0x201,
-  kErrKv8EmptyWait = 0x301,
-  kErrKv8FullWait = 0x302,
+  kErrKv8FullWait = 0x301,
 };
 
 // Constants of the split planner (mirrored by the decode kernel).
