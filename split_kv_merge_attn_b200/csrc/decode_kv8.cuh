@@ -11,7 +11,8 @@
 // times smaller), and ks, that power and log2(e) scale the fp32 logits.  For
 // P V the weights carry the block's scale: p_j vs_j is kept relative to its own
 // running maximum M >= x_j + log2 vs_j, apart from the softmax's m, so that the
-// fp16 weights use their range however much the scales of V differ.
+// fp16 weights use their range however much the scales of V differ.  Both
+// references follow the maxima loosely (within a factor of 2^8).
 //
 // What bounds it: bytes.  At HBM rate an SM receives about 23 codes per clock;
 // turning them into fp16 costs 1.25 (K) and 1.5 (V) lane instructions each,
@@ -30,6 +31,8 @@
 // and refills a stage as soon as it has read it, so there is no producer warp,
 // no barrier among warps until the end, and eight warps share an SM's registers.
 #pragma once
+
+#include <type_traits>
 
 #include "skv_device.cuh"
 #include "kv8.cuh"
@@ -52,7 +55,7 @@ struct Kv8DecodeCfg {
   static constexpr int kCombineBytes = 1024 + kKv8Warps * kKv8Rows * D * 4;
   static_assert(kRingBytes >= kCombineBytes, "the combine area reuses the ring");
   static constexpr int kQBytes = D == 256 ? kKv8Rows * D * 2 : 0;  // D = 256: Q fragments in shared memory
-  static constexpr int kSmemBytes = kRingBytes + kQBytes + kKv8Warps * kStages * 8 + 16 + 1024;
+  static constexpr int kSmemBytes = kRingBytes + kQBytes + kKv8Warps * 2 * kStages * 8 + 16 + 1024;
   static constexpr int kSteps = D / 16;                        // k-steps of Q K^T
   static constexpr int kTilesN = D / 8;                        // n-tiles of P V
   static constexpr int kGroups = kKeys / 16;                   // 16-key groups of a tile
@@ -123,9 +126,11 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
   const int warp = tid >> 5;
   const int lane = tid & 31;
   uint8_t* ring = smem + warp * Cfg::kStages * Cfg::kStageBytes;  // this warp's
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + Cfg::kRingBytes + Cfg::kQBytes) + warp * Cfg::kStages;
+  // arrival of the K tile, and of the V tile, of each stage
+  uint64_t* full_k = reinterpret_cast<uint64_t*>(smem + Cfg::kRingBytes + Cfg::kQBytes) + warp * 2 * Cfg::kStages;
+  uint64_t* full_v = full_k + Cfg::kStages;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::kRingBytes + Cfg::kQBytes +
-                                                             kKv8Warps * Cfg::kStages * 8);
+                                                             kKv8Warps * 2 * Cfg::kStages * 8);
   const int split = blockIdx.x;
   const int G = a.Hq / a.Hkv;
   const int rows_total = G * a.Lq;
@@ -134,7 +139,7 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
   const int b = blockIdx.y / (a.row_groups * a.Hkv);
 
   if (lane == 0) {
-    for (int s = 0; s < Cfg::kStages; ++s) mbar_init(&full[s], 1);
+    for (int s = 0; s < 2 * Cfg::kStages; ++s) mbar_init(&full_k[s], 1);
     fence_mbar_init();
   }
   if (tid == 0) *abort_flag = 0;
@@ -159,21 +164,21 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
   const int first = s0 + warp * kKeys;
   const int ntiles = first < s1 ? (s1 - first + kStride - 1) / kStride : 0;
 
-  // loads tile t into its stage (lane 0)
-  auto load = [&](int t) {
-    const int st = t % Cfg::kStages;
-    uint8_t* kt = ring + st * Cfg::kStageBytes;
-    uint8_t* vt = kt + Cfg::kTileBytes;
-    const int64_t token = bh * a.capacity + first + static_cast<int64_t>(t) * kStride;
+  // loads the K (V) tile whose first key is `key` into stage st (lane 0)
+  const int64_t token0 = bh * a.capacity;
+  auto load = [&](int key, int st, const CUtensorMap* map, int part, uint64_t* full) {
+    uint8_t* dst = ring + st * Cfg::kStageBytes + part * Cfg::kTileBytes;
+    const int64_t token = token0 + key;
     const int row = static_cast<int>(D == 64 ? token >> 1 : token);  // D = 64: two tokens in a 128-byte row
-    mbar_arrive_expect_tx(&full[st], Cfg::kStageBytes);
+    mbar_arrive_expect_tx(&full[st], Cfg::kTileBytes);
 #pragma unroll
-    for (int bx = 0; bx < Cfg::kBoxes; ++bx) tma_load_2d(kt + bx * kKeys * 128, &tmK, &full[st], bx * 128, row);
-#pragma unroll
-    for (int bx = 0; bx < Cfg::kBoxes; ++bx) tma_load_2d(vt + bx * kKeys * 128, &tmV, &full[st], bx * 128, row);
+    for (int bx = 0; bx < Cfg::kBoxes; ++bx) tma_load_2d(dst + bx * kKeys * 128, map, &full[st], bx * 128, row);
   };
   if (lane == 0) {
-    for (int t = 0; t < min(ntiles, Cfg::kStages); ++t) load(t);
+    for (int t = 0; t < min(ntiles, Cfg::kStages); ++t) {
+      load(first + t * kStride, t, &tmK, 0, full_k);
+      load(first + t * kStride, t, &tmV, 1, full_v);
+    }
   }
   __syncwarp();
 
@@ -267,30 +272,76 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
 
   const float* ksc = a.k_scale + bh * (a.capacity >> a.block_shift);
   const float* vsc = a.v_scale + bh * (a.capacity >> a.block_shift);
-  // 16 keys lie in one block of every block size: one scale each for a group.
-  // Scales are fetched one tile ahead; a group behind the last key has none.
+  // 16 keys lie in one block of every block size: one scale each for a group (the
+  // groups of a tile share it from blocks of 32 on).  Scales are fetched one tile
+  // ahead; a group behind the last key has none.
   float ks_next[Cfg::kGroups], vs_next[Cfg::kGroups];
   auto fetch_scales = [&](int key0) {
-#pragma unroll
-    for (int gr = 0; gr < Cfg::kGroups; ++gr) {
-      const int key = key0 + 16 * gr;
-      ks_next[gr] = key < s1 ? __ldg(ksc + (key >> a.block_shift)) : 0.f;
-      vs_next[gr] = key < s1 ? __ldg(vsc + (key >> a.block_shift)) : 0.f;
+    ks_next[0] = key0 < s1 ? __ldg(ksc + (key0 >> a.block_shift)) : 0.f;
+    vs_next[0] = key0 < s1 ? __ldg(vsc + (key0 >> a.block_shift)) : 0.f;
+    if constexpr (Cfg::kGroups == 2) {
+      ks_next[1] = ks_next[0];
+      vs_next[1] = vs_next[0];
+      if (a.block_shift == 4) {
+        ks_next[1] = key0 + 16 < s1 ? __ldg(ksc + (key0 >> 4) + 1) : 0.f;
+        vs_next[1] = key0 + 16 < s1 ? __ldg(vsc + (key0 >> 4) + 1) : 0.f;
+      }
     }
   };
   fetch_scales(first);
 
-  float m[2] = {-INFINITY, -INFINITY};    // running maximum of x
-  float mv[2] = {-INFINITY, -INFINITY};   // running maximum of x + log2 vs: O's unit is 2^mv
+  // m and mv are references a little behind the running maxima of x and of
+  // x + log2 vs: they move only when a value lies more than 2^kSlack above, so
+  // most tiles need no reduction over a row and no rescaling.  p and the fp16
+  // weights p vs / 2^mv then reach 2^kSlack, far from fp16's limit.
+  constexpr float kSlack = 8.f;
+  constexpr float kNone = -1.0e30f;  // nothing seen yet
+  float m[2] = {kNone, kNone};
+  float mv[2] = {kNone, kNone};
   float lsum[2] = {0.f, 0.f};
   float o[Cfg::kTilesN][4];
 #pragma unroll
   for (int j = 0; j < Cfg::kTilesN; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
 
-  int t = 0;
-  for (; t < ntiles; ++t) {
-    const int st = t % Cfg::kStages;
-    const int key0 = first + t * kStride;
+  constexpr int kNt = kKeys / 8;
+  // O += P V over one group of 16 keys, nvalid of them before the end
+  auto add_values = [&](uint32_t vt, int gr, const uint32_t (&pa)[4], int nvalid, auto partial) {
+#pragma unroll
+    for (int c = 0; c < D / 16; c += 2) {
+      // keys 0-7 and 8-15 of values 16 c .. 16 c + 15, then of the next 16
+      const uint32_t key = gr * 16 + (lane & 15);
+      const int cc = c + (lane >> 4);
+      uint32_t addr;
+      if constexpr (D == 64) addr = vt + sw128(key >> 1, (key & 1) * 4 + cc);
+      else addr = vt + (c / 8) * kKeys * 128 + sw128(key, cc % 8);
+      uint32_t v[4];
+      ldmatrix_x4_trans(addr, v[0], v[1], v[2], v[3]);
+      if constexpr (decltype(partial)::value) {
+        // codes behind the last key may be anything (unfilled cache, e4m3 NaN):
+        // their weight is 0 and so must the codes be
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int k0 = 2 * tq + 8 * (i & 1);  // this register's keys: k0 (low half), k0 + 1
+          v[i] &= (k0 < nvalid ? 0xffffu : 0u) | (k0 + 1 < nvalid ? 0xffff0000u : 0u);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t e0, o0, e1, o1;
+        codes_to_half_even_odd<kE4M3>(v[2 * i], e0, o0);
+        codes_to_half_even_odd<kE4M3>(v[2 * i + 1], e1, o1);
+        mma_16816<__half>(o[2 * (c + i)], pa, e0, e1);
+        mma_16816<__half>(o[2 * (c + i) + 1], pa, o0, o1);
+      }
+    }
+  };
+
+  int st = 0;
+  uint32_t phase = 0;
+  int key0 = first;
+  bool k_read = false;  // whether this tile's K has been read
+  for (; key0 < s1; key0 += kStride) {
+    const uint8_t* kt = ring + st * Cfg::kStageBytes;
     float ks[Cfg::kGroups], lv[Cfg::kGroups];
 #pragma unroll
     for (int gr = 0; gr < Cfg::kGroups; ++gr) {
@@ -298,12 +349,10 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
       lv[gr] = __log2f(vs_next[gr]);  // -inf for a block of zeros
     }
     fetch_scales(key0 + kStride);
-    if (!mbar_wait(&full[st], (t / Cfg::kStages) & 1, abort_flag, kErrKv8FullWait)) break;
-    const uint8_t* kt = ring + st * Cfg::kStageBytes;
-    const uint32_t vt = smem_u32(kt + Cfg::kTileBytes);
+    k_read = false;
+    if (!mbar_wait(&full_k[st], phase, abort_flag, kErrKv8FullWait)) break;
 
     // ---- S = Q K^T for 16 rows x kKeys keys; with two n-tiles only, two chains of MMAs each
-    constexpr int kNt = kKeys / 8;
     constexpr int kChains = kNt == 2 ? 2 : 1;
     float sc[kNt][kChains][4];
 #pragma unroll
@@ -343,17 +392,19 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
         }
       }
     }
+    k_read = true;
+    __syncwarp();  // the whole warp has read this K tile
+    if (lane == 0 && key0 + Cfg::kStages * kStride < s1) load(key0 + Cfg::kStages * kStride, st, &tmK, 0, full_k);
 
-    // ---- online softmax (exp2 domain), rows g and g + 8
+    // ---- softmax (exp2 domain), rows g and g + 8
     float x[kNt][4];
 #pragma unroll
     for (int nt = 0; nt < kNt; ++nt) {
-      const float f0 = xs0 * ks[nt / 2], f1 = xs1 * ks[nt / 2];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         float s = sc[nt][0][e];
         if constexpr (kChains == 2) s += sc[nt][1][e];
-        x[nt][e] = s * (e < 2 ? f0 : f1);
+        x[nt][e] = s * (ks[nt / 2] * (e < 2 ? xs0 : xs1));
       }
     }
     const bool masked = key0 + kKeys > safe_end;  // the same for the whole warp
@@ -377,37 +428,37 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
         }
       }
     }
-    float mx[2], vx[2];  // largest x, largest x + log2 vs
+    float mx[2], vx[2];  // this lane's largest x, largest x + log2 vs
 #pragma unroll
     for (int hr = 0; hr < 2; ++hr) {
-      float top[Cfg::kGroups];
 #pragma unroll
       for (int gr = 0; gr < Cfg::kGroups; ++gr) {
-        top[gr] = fmaxf(fmaxf(x[2 * gr][2 * hr], x[2 * gr][2 * hr + 1]),
-                        fmaxf(x[2 * gr + 1][2 * hr], x[2 * gr + 1][2 * hr + 1]));
+        const float top = fmaxf(fmax3(x[2 * gr][2 * hr], x[2 * gr][2 * hr + 1], x[2 * gr + 1][2 * hr]),
+                                x[2 * gr + 1][2 * hr + 1]);
+        mx[hr] = gr == 0 ? top : fmaxf(mx[hr], top);
+        vx[hr] = gr == 0 ? top + lv[gr] : fmaxf(vx[hr], top + lv[gr]);
       }
-      mx[hr] = top[0];
-      vx[hr] = top[0] + lv[0];
-      if constexpr (Cfg::kGroups == 2) {
-        mx[hr] = fmaxf(mx[hr], top[1]);
-        vx[hr] = fmaxf(vx[hr], top[1] + lv[1]);
-      }
-      mx[hr] = fmaxf(mx[hr], __shfl_xor_sync(0xffffffffu, mx[hr], 1));
-      vx[hr] = fmaxf(vx[hr], __shfl_xor_sync(0xffffffffu, vx[hr], 1));
-      mx[hr] = fmaxf(mx[hr], __shfl_xor_sync(0xffffffffu, mx[hr], 2));
-      vx[hr] = fmaxf(vx[hr], __shfl_xor_sync(0xffffffffu, vx[hr], 2));
     }
-    float mu[2], vu[2], al[2];
+    const bool above = mx[0] > m[0] + kSlack || mx[1] > m[1] + kSlack || vx[0] > mv[0] + kSlack || vx[1] > mv[1] + kSlack;
+    if (__any_sync(0xffffffffu, above)) {
 #pragma unroll
-    for (int hr = 0; hr < 2; ++hr) {
-      const float mn = fmaxf(m[hr], mx[hr]), vn = fmaxf(mv[hr], vx[hr]);
-      // exponents are taken against 0 while nothing has been seen
-      mu[hr] = mn == -INFINITY ? 0.f : mn;
-      vu[hr] = vn == -INFINITY ? 0.f : vn;
-      lsum[hr] *= ex2_approx(m[hr] - mu[hr]);
-      al[hr] = ex2_approx(mv[hr] - vu[hr]);
-      m[hr] = mn;
-      mv[hr] = vn;
+      for (int hr = 0; hr < 2; ++hr) {
+#pragma unroll
+        for (int sh = 1; sh < 4; sh <<= 1) {
+          mx[hr] = fmaxf(mx[hr], __shfl_xor_sync(0xffffffffu, mx[hr], sh));
+          vx[hr] = fmaxf(vx[hr], __shfl_xor_sync(0xffffffffu, vx[hr], sh));
+        }
+        const float mn = fmaxf(m[hr], mx[hr]), vn = fmaxf(mv[hr], vx[hr]);
+        lsum[hr] *= ex2_approx(m[hr] - mn);
+        const float al = ex2_approx(mv[hr] - vn);
+        m[hr] = mn;
+        mv[hr] = vn;
+#pragma unroll
+        for (int j = 0; j < Cfg::kTilesN; ++j) {
+          o[j][2 * hr] *= al;
+          o[j][2 * hr + 1] *= al;
+        }
+      }
     }
     uint32_t pa[Cfg::kGroups][4];
 #pragma unroll
@@ -417,7 +468,7 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
       float w[2];
 #pragma unroll
       for (int hr = 0; hr < 2; ++hr) {
-        w[hr] = ex2_approx(mu[hr] + lv[gr] - vu[hr]);
+        w[hr] = ex2_approx(m[hr] + lv[gr] - mv[hr]);
         w[hr] = w[hr] == INFINITY ? 3.0e38f : w[hr];
       }
 #pragma unroll
@@ -426,7 +477,7 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
         float pw[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float p = ex2_approx(x[nt][e] - mu[e >> 1]);
+          const float p = ex2_approx(x[nt][e] - m[e >> 1]);
           lsum[e >> 1] += p;
           pw[e] = p * w[e >> 1];
         }
@@ -438,56 +489,31 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
         pa[gr][2 * i + 1] = pack_f16x2(pw[2], pw[3]);
       }
     }
-    // the running maximum seldom moves after the first tiles
-    if (__any_sync(0xffffffffu, al[0] != 1.f || al[1] != 1.f)) {
-#pragma unroll
-      for (int j = 0; j < Cfg::kTilesN; ++j) {
-        o[j][0] *= al[0]; o[j][1] *= al[0];
-        o[j][2] *= al[1]; o[j][3] *= al[1];
-      }
-    }
 
-    // ---- O += P V, 16 keys at a time
+    if (!mbar_wait(&full_v[st], phase, abort_flag, kErrKv8FullWait)) break;
+    const uint32_t vt = smem_u32(kt + Cfg::kTileBytes);
+    if (key0 + kKeys <= s1) {
 #pragma unroll
-    for (int gr = 0; gr < Cfg::kGroups; ++gr) {
-      const int nvalid = s1 - key0 - 16 * gr;
-      if (gr > 0 && nvalid <= 0) break;
+      for (int gr = 0; gr < Cfg::kGroups; ++gr) add_values(vt, gr, pa[gr], 16, std::false_type{});
+    } else {
 #pragma unroll
-      for (int c = 0; c < D / 16; c += 2) {
-        // keys 0-7 and 8-15 of values 16 c .. 16 c + 15, then of the next 16
-        const uint32_t key = gr * 16 + (lane & 15);
-        const int cc = c + (lane >> 4);
-        uint32_t addr;
-        if constexpr (D == 64) addr = vt + sw128(key >> 1, (key & 1) * 4 + cc);
-        else addr = vt + (c / 8) * kKeys * 128 + sw128(key, cc % 8);
-        uint32_t v[4];
-        ldmatrix_x4_trans(addr, v[0], v[1], v[2], v[3]);
-        if (nvalid < 16) {
-          // codes behind the last key may be anything (unfilled cache, e4m3 NaN):
-          // their weight is 0 and so must the codes be
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int k0 = 2 * tq + 8 * (i & 1);  // this register's keys: k0 (low half), k0 + 1
-            v[i] &= (k0 < nvalid ? 0xffffu : 0u) | (k0 + 1 < nvalid ? 0xffff0000u : 0u);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint32_t e0, o0, e1, o1;
-          codes_to_half_even_odd<kE4M3>(v[2 * i], e0, o0);
-          codes_to_half_even_odd<kE4M3>(v[2 * i + 1], e1, o1);
-          mma_16816<__half>(o[2 * (c + i)], pa[gr], e0, e1);
-          mma_16816<__half>(o[2 * (c + i) + 1], pa[gr], o0, o1);
-        }
-      }
+      for (int gr = 0; gr < Cfg::kGroups; ++gr)
+        if (key0 + 16 * gr < s1) add_values(vt, gr, pa[gr], s1 - key0 - 16 * gr, std::true_type{});
     }
-    __syncwarp();  // the whole warp has read the stage
-    if (lane == 0 && t + Cfg::kStages < ntiles) load(t + Cfg::kStages);
+    __syncwarp();  // the whole warp has read this V tile
+    if (lane == 0 && key0 + Cfg::kStages * kStride < s1) load(key0 + Cfg::kStages * kStride, st, &tmV, 1, full_v);
+    if (++st == Cfg::kStages) {
+      st = 0;
+      phase ^= 1u;
+    }
   }
-  if (t < ntiles && lane == 0) {
+  if (key0 < s1 && lane == 0) {
     // a wait gave up: let the loads already issued land before the shared memory goes away
+    const int t = (key0 - first) / kStride, tk = t + (k_read ? 1 : 0);
+    for (int u = tk; u < min(ntiles, tk + Cfg::kStages); ++u)
+      mbar_drain(&full_k[u % Cfg::kStages], (u / Cfg::kStages) & 1, 20000000ull);
     for (int u = t; u < min(ntiles, t + Cfg::kStages); ++u)
-      mbar_drain(&full[u % Cfg::kStages], (u / Cfg::kStages) & 1, 20000000ull);
+      mbar_drain(&full_v[u % Cfg::kStages], (u / Cfg::kStages) & 1, 20000000ull);
   }
 
   // ---- combine the four warps' states
@@ -505,9 +531,9 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
   if (tq == 0) {
 #pragma unroll
     for (int hr = 0; hr < 2; ++hr) {
-      cm[warp * 16 + g + 8 * hr] = m[hr];
+      cm[warp * 16 + g + 8 * hr] = m[hr] == kNone ? -INFINITY : m[hr];
       cl[warp * 16 + g + 8 * hr] = lsum[hr];
-      cv[warp * 16 + g + 8 * hr] = mv[hr];
+      cv[warp * 16 + g + 8 * hr] = mv[hr] == kNone ? -INFINITY : mv[hr];
     }
   }
 #pragma unroll
