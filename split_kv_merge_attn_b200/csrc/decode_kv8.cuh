@@ -27,7 +27,7 @@
 // values 2g, 2g + 1 of two keys, which unpack into fragments of an even and an
 // odd n-tile.
 //
-// Each warp runs alone: it loads its own tiles (16 or 32 keys) into its own ring
+// Each warp runs alone: it loads its own tiles (16 to 64 keys) into its own ring
 // and refills a stage as soon as it has read it, so there is no producer warp,
 // no barrier among warps until the end, and eight warps share an SM's registers.
 #pragma once
@@ -45,12 +45,14 @@ constexpr int kKv8Rows = 16;
 
 template <int D>
 struct Kv8DecodeCfg {
-  static constexpr int kKeys = D == 256 ? 16 : 32;             // keys of a warp's tile
-  static constexpr int kTileBytes = kKeys * D;                 // one K or V tile
+  static constexpr int kKeys = D == 64 ? 64 : (D == 128 ? 32 : 16);  // keys of a load (4 KB of K, 4 KB of V)
+  static constexpr int kLoads = D == 128 ? 2 : 1;              // loads of one softmax tile
+  static constexpr int kTileKeys = kKeys * kLoads;
+  static constexpr int kTileBytes = kKeys * D;                 // one load of K or V
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kBoxes = D == 256 ? 2 : 1;              // 128-byte wide boxes
   static constexpr int kBoxRows = D == 64 ? kKeys / 2 : kKeys;
-  static constexpr int kStages = D == 64 ? 6 : 3;
+  static constexpr int kStages = 3;
   static constexpr int kRingBytes = kKv8Warps * kStages * kStageBytes;
   static constexpr int kCombineBytes = 1024 + kKv8Warps * kKv8Rows * D * 4;
   static_assert(kRingBytes >= kCombineBytes, "the combine area reuses the ring");
@@ -58,7 +60,7 @@ struct Kv8DecodeCfg {
   static constexpr int kSmemBytes = kRingBytes + kQBytes + kKv8Warps * 2 * kStages * 8 + 16 + 1024;
   static constexpr int kSteps = D / 16;                        // k-steps of Q K^T
   static constexpr int kTilesN = D / 8;                        // n-tiles of P V
-  static constexpr int kGroups = kKeys / 16;                   // 16-key groups of a tile
+  static constexpr int kGroups = kTileKeys / 16;               // 16-key groups of a tile
 };
 
 struct Kv8DecodeArgs {
@@ -97,6 +99,13 @@ __device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& h0, uint32_t
   }
 }
 
+// The smaller of two values, NaN if either is.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // The same with the pairs (a, c) and (b, d).
 template <bool kE4M3>
 __device__ __forceinline__ void codes_to_half_even_odd(uint32_t w, uint32_t& h0, uint32_t& h1) {
@@ -109,6 +118,46 @@ __device__ __forceinline__ void codes_to_half_even_odd(uint32_t w, uint32_t& h0,
     __half2 ha = __hsub2(*reinterpret_cast<__half2*>(&a), bias), hb = __hsub2(*reinterpret_cast<__half2*>(&b), bias);
     h0 = *reinterpret_cast<uint32_t*>(&ha);
     h1 = *reinterpret_cast<uint32_t*>(&hb);
+  }
+}
+
+// The weights of a tile from its scores s (x = s f): p = 2^(x - m), added to the
+// sums, and fp16 p vs / 2^mv, the A fragments of P V.
+template <int kGroups, bool kMasked>
+__device__ __forceinline__ void tile_weights(const float (&s)[2 * kGroups][4], const float (&f)[2][kGroups],
+                                             const float (&lv)[kGroups], const float (&m)[2], const float (&mv)[2],
+                                             float (&lsum)[2], uint32_t (&pa)[kGroups][4]) {
+#pragma unroll
+  for (int hr = 0; hr < 2; ++hr) {
+    uint64_t sum = f2_pack(0.f, 0.f);
+    const uint64_t minus_m = f2_pack(-m[hr], -m[hr]);
+#pragma unroll
+    for (int gr = 0; gr < kGroups; ++gr) {
+      // p vs / 2^mv = p * 2^(m + log2 vs - mv), kept finite where m lies far above
+      // the keys that set mv: their p is 0 then, and 0 * inf is not
+      const float w = min_nan(ex2_approx(m[hr] + lv[gr] - mv[hr]), 3.0e38f);
+      const uint64_t ww = f2_pack(w, w), ff = f2_pack(f[hr][gr], f[hr][gr]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float sa = s[2 * gr + i][2 * hr], sb = s[2 * gr + i][2 * hr + 1];
+        const float2 x = f2_unpack(ffma2(f2_pack(sa, sb), ff, minus_m));
+        float2 p = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+        if constexpr (kMasked) {  // a masked key's weight is 0 whatever its scales
+          p.x = sa == -INFINITY ? 0.f : p.x;
+          p.y = sb == -INFINITY ? 0.f : p.y;
+        }
+        const uint64_t pp = f2_pack(p.x, p.y);
+        sum = fadd2(sum, pp);
+        float2 pw = f2_unpack(fmul2(pp, ww));
+        if constexpr (kMasked) {
+          pw.x = sa == -INFINITY ? 0.f : pw.x;
+          pw.y = sb == -INFINITY ? 0.f : pw.y;
+        }
+        pa[gr][2 * i + hr] = pack_f16x2(pw.x, pw.y);
+      }
+    }
+    const float2 both = f2_unpack(sum);
+    lsum[hr] += both.x + both.y;
   }
 }
 
@@ -159,25 +208,28 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
     s1 = static_cast<int>(min(lo + C, static_cast<int64_t>(n)));
   }
   const int64_t bh = static_cast<int64_t>(b) * a.Hkv + hkv;
-  // this warp's tiles: keys first + t * kStride
-  constexpr int kStride = kKv8Warps * kKeys;
-  const int first = s0 + warp * kKeys;
+  // this warp's tiles: keys first + t * kStride; loads u = kLoads * t + i of their
+  // kKeys keys, the last ones of which may lie behind the end
+  constexpr int kTileKeys = Cfg::kTileKeys;
+  constexpr int kStride = kKv8Warps * kTileKeys;
+  const int first = s0 + warp * kTileKeys;
   const int ntiles = first < s1 ? (s1 - first + kStride - 1) / kStride : 0;
+  const int nloads = ntiles * Cfg::kLoads;
 
-  // loads the K (V) tile whose first key is `key` into stage st (lane 0)
-  const int64_t token0 = bh * a.capacity;
-  auto load = [&](int key, int st, const CUtensorMap* map, int part, uint64_t* full) {
+  // load u of K (part 0) or V (1) into its stage (lane 0)
+  const int64_t token0 = bh * a.capacity + first;
+  auto load = [&](int u, int st, const CUtensorMap* map, int part, uint64_t* full) {
     uint8_t* dst = ring + st * Cfg::kStageBytes + part * Cfg::kTileBytes;
-    const int64_t token = token0 + key;
+    const int64_t token = token0 + u / Cfg::kLoads * kStride + u % Cfg::kLoads * kKeys;
     const int row = static_cast<int>(D == 64 ? token >> 1 : token);  // D = 64: two tokens in a 128-byte row
     mbar_arrive_expect_tx(&full[st], Cfg::kTileBytes);
 #pragma unroll
     for (int bx = 0; bx < Cfg::kBoxes; ++bx) tma_load_2d(dst + bx * kKeys * 128, map, &full[st], bx * 128, row);
   };
   if (lane == 0) {
-    for (int t = 0; t < min(ntiles, Cfg::kStages); ++t) {
-      load(first + t * kStride, t, &tmK, 0, full_k);
-      load(first + t * kStride, t, &tmV, 1, full_v);
+    for (int u = 0; u < min(nloads, Cfg::kStages); ++u) {
+      load(u, u, &tmK, 0, full_k);
+      load(u, u, &tmV, 1, full_v);
     }
   }
   __syncwarp();
@@ -272,19 +324,22 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
 
   const float* ksc = a.k_scale + bh * (a.capacity >> a.block_shift);
   const float* vsc = a.v_scale + bh * (a.capacity >> a.block_shift);
-  // 16 keys lie in one block of every block size: one scale each for a group (the
-  // groups of a tile share it from blocks of 32 on).  Scales are fetched one tile
-  // ahead; a group behind the last key has none.
+  // 16 keys lie in one block of every block size: one scale each for a group.
+  // Scales are fetched one tile ahead; a group behind the last key has none.
   float ks_next[Cfg::kGroups], vs_next[Cfg::kGroups];
   auto fetch_scales = [&](int key0) {
     ks_next[0] = key0 < s1 ? __ldg(ksc + (key0 >> a.block_shift)) : 0.f;
     vs_next[0] = key0 < s1 ? __ldg(vsc + (key0 >> a.block_shift)) : 0.f;
-    if constexpr (Cfg::kGroups == 2) {
-      ks_next[1] = ks_next[0];
-      vs_next[1] = vs_next[0];
-      if (a.block_shift == 4) {
-        ks_next[1] = key0 + 16 < s1 ? __ldg(ksc + (key0 >> 4) + 1) : 0.f;
-        vs_next[1] = key0 + 16 < s1 ? __ldg(vsc + (key0 >> 4) + 1) : 0.f;
+#pragma unroll
+    for (int gr = 1; gr < Cfg::kGroups; ++gr) {
+      ks_next[gr] = ks_next[gr - 1];
+      vs_next[gr] = vs_next[gr - 1];
+      // a new block every 1 << (block_shift - 4) groups (tiles begin at a block's
+      // begin, or lie inside one)
+      if ((gr & ((1 << (a.block_shift - 4)) - 1)) == 0) {
+        const int key = key0 + 16 * gr;
+        ks_next[gr] = key < s1 ? __ldg(ksc + (key >> a.block_shift)) : 0.f;
+        vs_next[gr] = key < s1 ? __ldg(vsc + (key >> a.block_shift)) : 0.f;
       }
     }
   };
@@ -303,7 +358,7 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
 #pragma unroll
   for (int j = 0; j < Cfg::kTilesN; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
 
-  constexpr int kNt = kKeys / 8;
+  constexpr int kNt = kTileKeys / 8;
   // O += P V over one group of 16 keys, nvalid of them before the end
   auto add_values = [&](uint32_t vt, int gr, const uint32_t (&pa)[4], int nvalid, auto partial) {
 #pragma unroll
@@ -336,95 +391,110 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
     }
   };
 
-  int st = 0;
-  uint32_t phase = 0;
-  int key0 = first;
-  bool k_read = false;  // whether this tile's K has been read
-  for (; key0 < s1; key0 += kStride) {
-    const uint8_t* kt = ring + st * Cfg::kStageBytes;
-    float ks[Cfg::kGroups], lv[Cfg::kGroups];
+  // the warp gives up as one: a lane whose limit expires takes the others along
+  auto wait = [&](uint64_t* full, uint32_t phase) {
+    return __all_sync(0xffffffffu, mbar_wait(full, phase, abort_flag, kErrKv8FullWait)) != 0;
+  };
+  int st_k = 0, st_v = 0;
+  uint32_t phase_k = 0, phase_v = 0;
+  int uk = 0, uv = 0;  // loads of K and of V read so far
+  bool ok = true;
+  for (int key0 = first; key0 < s1; key0 += kStride) {
+    float f[2][Cfg::kGroups], lv[Cfg::kGroups];
 #pragma unroll
     for (int gr = 0; gr < Cfg::kGroups; ++gr) {
-      ks[gr] = ks_next[gr];
+      f[0][gr] = xs0 * ks_next[gr];
+      f[1][gr] = xs1 * ks_next[gr];
       lv[gr] = __log2f(vs_next[gr]);  // -inf for a block of zeros
     }
     fetch_scales(key0 + kStride);
-    k_read = false;
-    if (!mbar_wait(&full_k[st], phase, abort_flag, kErrKv8FullWait)) break;
 
-    // ---- S = Q K^T for 16 rows x kKeys keys; with two n-tiles only, two chains of MMAs each
-    constexpr int kChains = kNt == 2 ? 2 : 1;
-    float sc[kNt][kChains][4];
+    // ---- S = Q K^T for 16 rows x kTileKeys keys
+    float s[kNt][4];
 #pragma unroll
-    for (int nt = 0; nt < kNt; ++nt)
+    for (int ld = 0; ld < Cfg::kLoads; ++ld) {
+      ok = ok && wait(&full_k[st_k], phase_k);
+      if (!ok) continue;
+      const uint8_t* kt = ring + st_k * Cfg::kStageBytes;
+      constexpr int kN = kKeys / 8;              // n-tiles of a load
+      constexpr int kChains = kN == 2 ? 2 : 1;   // with two n-tiles only, two chains of MMAs each
+      float sc[kN][kChains][4];
 #pragma unroll
-      for (int i = 0; i < kChains; ++i) sc[nt][i][0] = sc[nt][i][1] = sc[nt][i][2] = sc[nt][i][3] = 0.f;
+      for (int nt = 0; nt < kN; ++nt)
 #pragma unroll
-    for (int bx = 0; bx < Cfg::kBoxes; ++bx) {
+        for (int i = 0; i < kChains; ++i) sc[nt][i][0] = sc[nt][i][1] = sc[nt][i][2] = sc[nt][i][3] = 0.f;
 #pragma unroll
-      for (int half = 0; half < (D == 64 ? 1 : 2); ++half) {
-        uint4 kw[kNt];
+      for (int bx = 0; bx < Cfg::kBoxes; ++bx) {
 #pragma unroll
-        for (int nt = 0; nt < kNt; ++nt) {
-          const uint32_t key = nt * 8 + g;
-          uint32_t off;
-          if constexpr (D == 64) off = sw128(key >> 1, (key & 1) * 4 + tq);
-          else off = bx * kKeys * 128 + sw128(key, 2 * tq + half);
-          kw[nt] = *reinterpret_cast<const uint4*>(kt + off);
-        }
+        for (int half = 0; half < (D == 64 ? 1 : 2); ++half) {
+          uint4 kw[kN];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int kk = bx * 8 + half * 4 + i;
-          uint32_t aq[4];
-          if constexpr (D == 256) {
-            const uint4 u = qfrag[kk * 32 + lane];
-            aq[0] = u.x; aq[1] = u.y; aq[2] = u.z; aq[3] = u.w;
-          } else {
-            aq[0] = qa[kk][0]; aq[1] = qa[kk][1]; aq[2] = qa[kk][2]; aq[3] = qa[kk][3];
+          for (int nt = 0; nt < kN; ++nt) {
+            const uint32_t key = nt * 8 + g;
+            uint32_t off;
+            if constexpr (D == 64) off = sw128(key >> 1, (key & 1) * 4 + tq);
+            else off = bx * kKeys * 128 + sw128(key, 2 * tq + half);
+            kw[nt] = *reinterpret_cast<const uint4*>(kt + off);
           }
 #pragma unroll
-          for (int nt = 0; nt < kNt; ++nt) {
-            const uint32_t w = i == 0 ? kw[nt].x : (i == 1 ? kw[nt].y : (i == 2 ? kw[nt].z : kw[nt].w));
-            uint32_t b0, b1;
-            codes_to_half<kE4M3>(w, b0, b1);
-            mma_16816<__half>(sc[nt][i % kChains], aq, b0, b1);
+          for (int i = 0; i < 4; ++i) {
+            const int kk = bx * 8 + half * 4 + i;
+            uint32_t aq[4];
+            if constexpr (D == 256) {
+              const uint4 u = qfrag[kk * 32 + lane];
+              aq[0] = u.x; aq[1] = u.y; aq[2] = u.z; aq[3] = u.w;
+            } else {
+              aq[0] = qa[kk][0]; aq[1] = qa[kk][1]; aq[2] = qa[kk][2]; aq[3] = qa[kk][3];
+            }
+#pragma unroll
+            for (int nt = 0; nt < kN; ++nt) {
+              const uint32_t w = i == 0 ? kw[nt].x : (i == 1 ? kw[nt].y : (i == 2 ? kw[nt].z : kw[nt].w));
+              uint32_t b0, b1;
+              codes_to_half<kE4M3>(w, b0, b1);
+              mma_16816<__half>(sc[nt][i % kChains], aq, b0, b1);
+            }
           }
         }
       }
+      __syncwarp();  // the whole warp has read this load
+      if (lane == 0 && uk + Cfg::kStages < nloads) load(uk + Cfg::kStages, st_k, &tmK, 0, full_k);
+      ++uk;
+      if (++st_k == Cfg::kStages) {
+        st_k = 0;
+        phase_k ^= 1u;
+      }
+#pragma unroll
+      for (int nt = 0; nt < kN; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[ld * kN + nt][e] = sc[nt][0][e];
+          if constexpr (kChains == 2) s[ld * kN + nt][e] += sc[nt][1][e];
+        }
     }
-    k_read = true;
-    __syncwarp();  // the whole warp has read this K tile
-    if (lane == 0 && key0 + Cfg::kStages * kStride < s1) load(key0 + Cfg::kStages * kStride, st, &tmK, 0, full_k);
+    if (!ok) break;
 
     // ---- softmax (exp2 domain), rows g and g + 8
-    float x[kNt][4];
-#pragma unroll
-    for (int nt = 0; nt < kNt; ++nt) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float s = sc[nt][0][e];
-        if constexpr (kChains == 2) s += sc[nt][1][e];
-        x[nt][e] = s * (ks[nt / 2] * (e < 2 ? xs0 : xs1));
-      }
-    }
-    const bool masked = key0 + kKeys > safe_end;  // the same for the whole warp
+    const bool masked = key0 + kTileKeys > safe_end;  // the same for the whole warp
     if (masked) {
 #pragma unroll
       for (int nt = 0; nt < kNt; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (key0 + nt * 8 + 2 * tq + (e & 1) >= row_end[e >> 1]) x[nt][e] = -INFINITY;
+          if (key0 + nt * 8 + 2 * tq + (e & 1) >= row_end[e >> 1]) s[nt][e] = -INFINITY;
     }
     if constexpr (kLogits) {
       // up to 16-key alignment the slots behind the last key are this warp's too
-      // (-inf there); the capacity is a multiple of 16
+      // (nothing reads them); the capacity is a multiple of 16
 #pragma unroll
       for (int hr = 0; hr < 2; ++hr) {
         if (lrow[hr] != nullptr) {
 #pragma unroll
           for (int nt = 0; nt < kNt; ++nt)
-            if (nt < 2 || key0 + 16 < s1)
-              *reinterpret_cast<float2*>(lrow[hr] + key0 + nt * 8 + 2 * tq) = make_float2(x[nt][2 * hr], x[nt][2 * hr + 1]);
+            if (key0 + nt / 2 * 16 < s1) {
+              const float sa = s[nt][2 * hr], sb = s[nt][2 * hr + 1], fx = f[hr][nt / 2];
+              *reinterpret_cast<float2*>(lrow[hr] + key0 + nt * 8 + 2 * tq) =
+                  make_float2(masked && sa == -INFINITY ? sa : sa * fx, masked && sb == -INFINITY ? sb : sb * fx);
+            }
         }
       }
     }
@@ -433,8 +503,8 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
     for (int hr = 0; hr < 2; ++hr) {
 #pragma unroll
       for (int gr = 0; gr < Cfg::kGroups; ++gr) {
-        const float top = fmaxf(fmax3(x[2 * gr][2 * hr], x[2 * gr][2 * hr + 1], x[2 * gr + 1][2 * hr]),
-                                x[2 * gr + 1][2 * hr + 1]);
+        const float top = fmaxf(fmax3(s[2 * gr][2 * hr], s[2 * gr][2 * hr + 1], s[2 * gr + 1][2 * hr]),
+                                s[2 * gr + 1][2 * hr + 1]) * f[hr][gr];
         mx[hr] = gr == 0 ? top : fmaxf(mx[hr], top);
         vx[hr] = gr == 0 ? top + lv[gr] : fmaxf(vx[hr], top + lv[gr]);
       }
@@ -461,58 +531,40 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
       }
     }
     uint32_t pa[Cfg::kGroups][4];
-#pragma unroll
-    for (int gr = 0; gr < Cfg::kGroups; ++gr) {
-      // p vs / 2^mv = p * 2^(m + log2 vs - mv), kept finite where m lies far above
-      // the keys that set mv: their p is 0 then, and 0 * inf is not
-      float w[2];
-#pragma unroll
-      for (int hr = 0; hr < 2; ++hr) {
-        w[hr] = ex2_approx(m[hr] + lv[gr] - mv[hr]);
-        w[hr] = w[hr] == INFINITY ? 3.0e38f : w[hr];
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int nt = 2 * gr + i;
-        float pw[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float p = ex2_approx(x[nt][e] - m[e >> 1]);
-          lsum[e >> 1] += p;
-          pw[e] = p * w[e >> 1];
-        }
-        if (masked) {  // a masked key's weight is 0 whatever its scale
-#pragma unroll
-          for (int e = 0; e < 4; ++e) pw[e] = x[nt][e] == -INFINITY ? 0.f : pw[e];
-        }
-        pa[gr][2 * i] = pack_f16x2(pw[0], pw[1]);
-        pa[gr][2 * i + 1] = pack_f16x2(pw[2], pw[3]);
-      }
-    }
+    if (masked) tile_weights<Cfg::kGroups, true>(s, f, lv, m, mv, lsum, pa);
+    else tile_weights<Cfg::kGroups, false>(s, f, lv, m, mv, lsum, pa);
 
-    if (!mbar_wait(&full_v[st], phase, abort_flag, kErrKv8FullWait)) break;
-    const uint32_t vt = smem_u32(kt + Cfg::kTileBytes);
-    if (key0 + kKeys <= s1) {
+    // ---- O += P V
 #pragma unroll
-      for (int gr = 0; gr < Cfg::kGroups; ++gr) add_values(vt, gr, pa[gr], 16, std::false_type{});
-    } else {
+    for (int ld = 0; ld < Cfg::kLoads; ++ld) {
+      ok = ok && wait(&full_v[st_v], phase_v);
+      if (!ok) continue;
+      const uint32_t vt = smem_u32(ring + st_v * Cfg::kStageBytes + Cfg::kTileBytes);
+      const int key1 = key0 + ld * kKeys;
+      if (key1 + kKeys <= s1) {
 #pragma unroll
-      for (int gr = 0; gr < Cfg::kGroups; ++gr)
-        if (key0 + 16 * gr < s1) add_values(vt, gr, pa[gr], s1 - key0 - 16 * gr, std::true_type{});
+        for (int gr = 0; gr < kKeys / 16; ++gr) add_values(vt, gr, pa[ld * (kKeys / 16) + gr], 16, std::false_type{});
+      } else {
+#pragma unroll
+        for (int gr = 0; gr < kKeys / 16; ++gr)
+          if (key1 + 16 * gr < s1)
+            add_values(vt, gr, pa[ld * (kKeys / 16) + gr], s1 - key1 - 16 * gr, std::true_type{});
+      }
+      __syncwarp();  // the whole warp has read this load
+      if (lane == 0 && uv + Cfg::kStages < nloads) load(uv + Cfg::kStages, st_v, &tmV, 1, full_v);
+      ++uv;
+      if (++st_v == Cfg::kStages) {
+        st_v = 0;
+        phase_v ^= 1u;
+      }
     }
-    __syncwarp();  // the whole warp has read this V tile
-    if (lane == 0 && key0 + Cfg::kStages * kStride < s1) load(key0 + Cfg::kStages * kStride, st, &tmV, 1, full_v);
-    if (++st == Cfg::kStages) {
-      st = 0;
-      phase ^= 1u;
-    }
+    if (!ok) break;
   }
-  if (key0 < s1 && lane == 0) {
+  if (uv < nloads && lane == 0) {
     // a wait gave up: let the loads already issued land before the shared memory goes away
-    const int t = (key0 - first) / kStride, tk = t + (k_read ? 1 : 0);
-    for (int u = tk; u < min(ntiles, tk + Cfg::kStages); ++u)
+    for (int u = uk; u < min(nloads, uk + Cfg::kStages); ++u)
       mbar_drain(&full_k[u % Cfg::kStages], (u / Cfg::kStages) & 1, 20000000ull);
-    for (int u = t; u < min(ntiles, t + Cfg::kStages); ++u)
+    for (int u = uv; u < min(nloads, uv + Cfg::kStages); ++u)
       mbar_drain(&full_v[u % Cfg::kStages], (u / Cfg::kStages) & 1, 20000000ull);
   }
 
