@@ -324,26 +324,20 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
 
   const float* ksc = a.k_scale + bh * (a.capacity >> a.block_shift);
   const float* vsc = a.v_scale + bh * (a.capacity >> a.block_shift);
-  // 16 keys lie in one block of every block size: one scale each for a group.
-  // Scales are fetched one tile ahead; a group behind the last key has none.
-  float ks_next[Cfg::kGroups], vs_next[Cfg::kGroups];
+  // 16 keys lie in one block of every block size, so a tile has one pair of scales
+  // for each group of 16.  A lane holds those of one group of the next 32 / kGroups
+  // tiles (0 for a group behind the last key), loaded that many tiles ahead: under
+  // load a scale takes longer to arrive than a tile to compute (one tile ahead cost
+  // 1.2 us of 31 at D = 128, 15 us of 110 at D = 64).
+  constexpr int kChunk = 32 / Cfg::kGroups;  // tiles of a chunk
+  float ks_chunk = 0.f, lv_chunk = 0.f, ks_ahead = 0.f, vs_ahead = 0.f;
   auto fetch_scales = [&](int key0) {
-    ks_next[0] = key0 < s1 ? __ldg(ksc + (key0 >> a.block_shift)) : 0.f;
-    vs_next[0] = key0 < s1 ? __ldg(vsc + (key0 >> a.block_shift)) : 0.f;
-#pragma unroll
-    for (int gr = 1; gr < Cfg::kGroups; ++gr) {
-      ks_next[gr] = ks_next[gr - 1];
-      vs_next[gr] = vs_next[gr - 1];
-      // a new block every 1 << (block_shift - 4) groups (tiles begin at a block's
-      // begin, or lie inside one)
-      if ((gr & ((1 << (a.block_shift - 4)) - 1)) == 0) {
-        const int key = key0 + 16 * gr;
-        ks_next[gr] = key < s1 ? __ldg(ksc + (key >> a.block_shift)) : 0.f;
-        vs_next[gr] = key < s1 ? __ldg(vsc + (key >> a.block_shift)) : 0.f;
-      }
-    }
+    const int64_t key = key0 + static_cast<int64_t>(lane / Cfg::kGroups) * kStride + lane % Cfg::kGroups * 16;
+    ks_ahead = key < s1 ? __ldg(ksc + (key >> a.block_shift)) : 0.f;
+    vs_ahead = key < s1 ? __ldg(vsc + (key >> a.block_shift)) : 0.f;
   };
   fetch_scales(first);
+  int chunk_tile = 0;  // the current tile's place in its chunk
 
   // m and mv are references a little behind the running maxima of x and of
   // x + log2 vs: they move only when a value lies more than 2^kSlack above, so
@@ -400,14 +394,20 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
   int uk = 0, uv = 0;  // loads of K and of V read so far
   bool ok = true;
   for (int key0 = first; key0 < s1; key0 += kStride) {
+    if (chunk_tile == 0) {
+      ks_chunk = ks_ahead;
+      lv_chunk = __log2f(vs_ahead);  // -inf for a block of zeros
+      fetch_scales(key0 + kChunk * kStride);
+    }
     float f[2][Cfg::kGroups], lv[Cfg::kGroups];
 #pragma unroll
     for (int gr = 0; gr < Cfg::kGroups; ++gr) {
-      f[0][gr] = xs0 * ks_next[gr];
-      f[1][gr] = xs1 * ks_next[gr];
-      lv[gr] = __log2f(vs_next[gr]);  // -inf for a block of zeros
+      const float ks = __shfl_sync(0xffffffffu, ks_chunk, chunk_tile * Cfg::kGroups + gr);
+      lv[gr] = __shfl_sync(0xffffffffu, lv_chunk, chunk_tile * Cfg::kGroups + gr);
+      f[0][gr] = xs0 * ks;
+      f[1][gr] = xs1 * ks;
     }
-    fetch_scales(key0 + kStride);
+    chunk_tile = (chunk_tile + 1) % kChunk;
 
     // ---- S = Q K^T for 16 rows x kTileKeys keys
     float s[kNt][4];
