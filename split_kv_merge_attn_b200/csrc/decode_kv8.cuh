@@ -676,15 +676,24 @@ __global__ void __launch_bounds__(256) kv8_weights_kernel(const Kv8WeightArgs a)
   const float* x = a.logits + bh * a.rows * a.capacity + j;
   const float* lse = a.lse + bh * a.rows;
   float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int r = 0; r < a.rows; ++r) {
-    const float4 v = *reinterpret_cast<const float4*>(x + static_cast<int64_t>(r) * a.capacity);
-    const float L = lse[r];
-    if (L == -INFINITY) continue;  // no visible key
-    s[0] += ex2_approx(v.x - L);
-    s[1] += ex2_approx(v.y - L);
-    s[2] += ex2_approx(v.z - L);
-    s[3] += ex2_approx(v.w - L);
+  // eight rows in flight
+  for (int r0 = 0; r0 < a.rows; r0 += 8) {
+    float4 v[8];
+    float L[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = min(r0 + i, a.rows - 1);
+      v[i] = *reinterpret_cast<const float4*>(x + static_cast<int64_t>(r) * a.capacity);
+      L[i] = r0 + i < a.rows ? lse[r] : -INFINITY;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (L[i] == -INFINITY) continue;  // no visible key (or no such row)
+      s[0] += ex2_approx(v[i].x - L[i]);
+      s[1] += ex2_approx(v[i].y - L[i]);
+      s[2] += ex2_approx(v[i].z - L[i]);
+      s[3] += ex2_approx(v[i].w - L[i]);
+    }
   }
   float* w = a.weights + bh * a.capacity + j;
   if (j + 4 <= n) {

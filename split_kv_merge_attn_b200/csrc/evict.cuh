@@ -22,6 +22,7 @@ namespace skv {
 constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kEvictBins = 256;
+constexpr int kEvictChunk = 8;  // keys a lane holds
 
 struct EvictArgs {
   const float* weights;      // [B, Hkv, capacity]
@@ -33,13 +34,13 @@ struct EvictArgs {
   uint8_t* to_codes[2];
   float* to_scale[2];
   float* to_weights;         // [B, Hkv, to_capacity]
-  int B, Hkv, D, capacity, to_capacity, block_shift, budget, sink, recent;
+  int B, Hkv, capacity, to_capacity, block_shift, budget, sink, recent;
 };
 
 __device__ __forceinline__ uint32_t weight_key(float w) {
-  if (isnan(w)) return 0u;
+  if (isnan(w)) return 1u;
   const uint32_t u = __float_as_uint(w + 0.f);  // -0 -> +0
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);   // >= 0x007fffff for -inf
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);   // >= 0x007fffff (that of -inf)
 }
 
 __device__ __forceinline__ uint32_t cluster_ctarank() {
@@ -86,14 +87,28 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const Evict
   const int wanted = a.budget - a.sink - a.recent;
   const float* w = a.weights + bh * a.capacity;
 
-  // this CTA's candidates, and this warp's (in order, whole warps of 32)
+  // this CTA's candidates, and this warp's (in order), in chunks of 256 to a warp
   const int per_cta = ((hi - lo + static_cast<int>(parts) - 1) / static_cast<int>(parts) + 31) / 32 * 32;
   const int c0 = min(lo + static_cast<int>(rank) * per_cta, hi), c1 = min(c0 + per_cta, hi);
   const int per_warp = ((c1 - c0 + kEvictWarps - 1) / kEvictWarps + 31) / 32 * 32;
   const int w0 = min(c0 + warp * per_warp, c1), w1 = min(w0 + per_warp, c1);
+  // keys j, j + 32, ... of a chunk in a lane; 0 (below every weight's) behind the
+  // end, where NaN is 1.  A warp of one chunk keeps it in registers.
+  uint32_t key[kEvictChunk];
+  auto load = [&](int j) {
+    float x[kEvictChunk];
+#pragma unroll
+    for (int i = 0; i < kEvictChunk; ++i) x[i] = j + 32 * i + lane < w1 ? __ldg(w + j + 32 * i + lane) : 0.f;
+#pragma unroll
+    for (int i = 0; i < kEvictChunk; ++i) key[i] = j + 32 * i + lane < w1 ? weight_key(x[i]) : 0u;
+  };
+  const bool one_chunk = w1 - w0 <= 32 * kEvictChunk;
+  load(w0);
 
-  __shared__ uint32_t hist[kEvictBins];      // read by the whole cluster
-  __shared__ uint32_t sums[kEvictBins];      // the cluster's histogram
+  constexpr int kCopies = 4;  // histograms of a CTA, by lane: fewer lanes meet at a bin
+  __shared__ uint32_t hist[kCopies][kEvictBins];
+  __shared__ uint32_t sums[4][kEvictBins];   // the CTA's, one for each pass: read by the whole cluster
+  __shared__ uint32_t all[kEvictBins];       // the cluster's
   __shared__ uint32_t found[2];              // bin, candidates above it
   __shared__ uint32_t counts[2];             // this CTA's kept: above the threshold, equal to it
   __shared__ uint32_t warp_counts[2][kEvictWarps];
@@ -101,27 +116,41 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const Evict
   uint32_t prefix = 0;
   uint32_t rest = static_cast<uint32_t>(wanted);  // still to take among those that share the prefix
   if (wanted > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = tid; i < kEvictBins; i += kEvictThreads) hist[i] = 0;
+#pragma unroll 1
+    for (int pass = 0; pass < 4; ++pass) {
+      const int shift = 24 - 8 * pass;
+      for (int i = tid; i < kCopies * kEvictBins; i += kEvictThreads) hist[0][i] = 0;
       __syncthreads();
-      for (int j = c0 + tid; j < c1; j += kEvictThreads) {
-        const uint32_t k = weight_key(__ldg(w + j));
-        if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255u], 1u);
+      for (int j = w0; j < w1; j += 32 * kEvictChunk) {
+        if (!one_chunk) load(j);
+#pragma unroll
+        for (int i = 0; i < kEvictChunk; ++i) {
+          const uint32_t k = key[i];
+          if (k != 0 && (pass == 0 || ((k ^ prefix) >> (shift + 8)) == 0))
+            atomicAdd(&hist[lane % kCopies][(k >> shift) & 255u], 1u);
+        }
+      }
+      __syncthreads();
+      if (tid < kEvictBins) {
+        uint32_t t = 0;
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) t += hist[i][tid];
+        sums[pass][tid] = t;
       }
       cluster_barrier();
       if (tid < kEvictBins) {
-        uint32_t s = 0;
-        for (uint32_t r = 0; r < parts; ++r) s += ld_cluster_u32(&hist[tid], r);
-        sums[tid] = s;
+        uint32_t t = 0;
+        for (uint32_t r = 0; r < parts; ++r) t += ld_cluster_u32(&sums[pass][tid], r);
+        all[tid] = t;
       }
-      cluster_barrier();  // every CTA has read the histograms before they are cleared
+      __syncthreads();
       if (warp == 0) {
         // lane l holds bins 255 - 8 l .. 248 - 8 l, from the top
-        uint32_t s[8], mine = 0;
+        uint32_t t[8], mine = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          s[i] = sums[255 - 8 * lane - i];
-          mine += s[i];
+          t[i] = all[255 - 8 * lane - i];
+          mine += t[i];
         }
         uint32_t before = mine;
 #pragma unroll
@@ -134,28 +163,30 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const Evict
           uint32_t above = before;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            if (above < rest && above + s[i] >= rest) {
+            if (above < rest && above + t[i] >= rest) {
               found[0] = static_cast<uint32_t>(255 - 8 * lane - i);
               found[1] = above;
             }
-            above += s[i];
+            above += t[i];
           }
         }
       }
       __syncthreads();
       prefix |= found[0] << shift;
       rest -= found[1];
-      __syncthreads();
     }
   }
   const uint32_t threshold = prefix;
   // kept candidates: key > threshold, and the first `rest` of those equal to it
   uint32_t above = 0, equal = 0;
   if (wanted > 0) {
-    for (int j = w0 + lane; j < w1; j += 32) {
-      const uint32_t k = weight_key(__ldg(w + j));
-      above += k > threshold;
-      equal += k == threshold;
+    for (int j = w0; j < w1; j += 32 * kEvictChunk) {
+      if (!one_chunk) load(j);
+#pragma unroll
+      for (int i = 0; i < kEvictChunk; ++i) {
+        above += key[i] > threshold;
+        equal += key[i] == threshold;
+      }
     }
     above = __reduce_add_sync(0xffffffffu, above);
     equal = __reduce_add_sync(0xffffffffu, equal);
@@ -166,9 +197,9 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const Evict
   }
   __syncthreads();
   if (tid < 2) {
-    uint32_t s = 0;
-    for (int i = 0; i < kEvictWarps; ++i) s += warp_counts[tid][i];
-    counts[tid] = s;
+    uint32_t t = 0;
+    for (int i = 0; i < kEvictWarps; ++i) t += warp_counts[tid][i];
+    counts[tid] = t;
   }
   cluster_barrier();
   uint32_t place = 0, seen = 0;  // candidates above / equal before this warp's
@@ -176,7 +207,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const Evict
     place += ld_cluster_u32(&counts[0], r);
     seen += ld_cluster_u32(&counts[1], r);
   }
-  cluster_barrier();  // nobody leaves while its counts may be read
+  cluster_barrier();  // nobody leaves while its counts or histograms may be read
   for (int i = 0; i < warp; ++i) {
     place += warp_counts[0][i];
     seen += warp_counts[1][i];
@@ -184,17 +215,19 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const Evict
   if (wanted > 0) {
     // place: candidates kept before this one
     place += min(seen, rest);
-    for (int j = w0; j < w1; j += 32) {
-      const int jj = j + lane;
-      const uint32_t k = jj < w1 ? weight_key(__ldg(w + jj)) : 0u;
-      const bool eq = jj < w1 && k == threshold;
-      const uint32_t eq_mask = __ballot_sync(0xffffffffu, eq);
-      const uint32_t below = (1u << lane) - 1u;
-      const bool take = (jj < w1 && k > threshold) || (eq && seen + __popc(eq_mask & below) < rest);
-      const uint32_t mask = __ballot_sync(0xffffffffu, take);
-      if (take) kept[a.sink + static_cast<int>(place) + __popc(mask & below)] = jj;
-      place += __popc(mask);
-      seen += __popc(eq_mask);
+    const uint32_t below = (1u << lane) - 1u;
+    for (int j = w0; j < w1; j += 32 * kEvictChunk) {
+      if (!one_chunk) load(j);
+#pragma unroll
+      for (int i = 0; i < kEvictChunk; ++i) {
+        const bool eq = key[i] == threshold;
+        const uint32_t eq_mask = __ballot_sync(0xffffffffu, eq);
+        const bool take = key[i] > threshold || (eq && seen + __popc(eq_mask & below) < rest);
+        const uint32_t mask = __ballot_sync(0xffffffffu, take);
+        if (take) kept[a.sink + static_cast<int>(place) + __popc(mask & below)] = j + 32 * i + lane;
+        place += __popc(mask);
+        seen += __popc(eq_mask);
+      }
     }
   }
   for (int i = static_cast<int>(rank) * kEvictThreads + tid; i < a.sink; i += kEvictThreads * static_cast<int>(parts)) kept[i] = i;
@@ -204,10 +237,13 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const Evict
 
 // Compaction: one warp per 16 kept tokens of one (batch entry, head), K and V;
 // blocks larger than 16 tokens share their scale through shared memory.
-// Bound by bytes: the kept tokens' codes in and out.
-template <bool kE4M3>
+// Bound by bytes: the kept tokens' codes in and out.  The codes are requested
+// before the scales are known, all of a warp's at once.
+template <int D, bool kE4M3>
 __global__ void __launch_bounds__(256) evict_move_kernel(const EvictArgs a) {
   using Code = Kv8Code<kE4M3>;
+  constexpr int kUnits = D / 16;              // 16-byte pieces of a row
+  constexpr int kIters = 16 * kUnits / 32;    // pieces a lane moves of K, and of V
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t bh = blockIdx.y;
@@ -222,6 +258,16 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const EvictArgs a) {
   const int which_lane = lane >> 4;  // lanes 0-15: K's scales, 16-31: V's
   const float* scale = a.scale[which_lane] + bh * (a.capacity >> a.block_shift);
   const float s_tok = from >= 0 ? scale[from >> a.block_shift] : 0.f;
+  uint4 v[2][kIters];
+#pragma unroll
+  for (int which = 0; which < 2; ++which)
+#pragma unroll
+    for (int i = 0; i < kIters; ++i) {
+      const int t = (i * 32 + lane) / kUnits, c = (i * 32 + lane) % kUnits;
+      const int f = __shfl_sync(0xffffffffu, from, t);
+      v[which][i] = make_uint4(0, 0, 0, 0);
+      if (f >= 0) v[which][i] = __ldg(reinterpret_cast<const uint4*>(a.codes[which] + (bh * a.capacity + f) * D) + c);
+    }
   // magnitude bits: scales are >= 0, and NaN must win
   uint32_t top = __float_as_uint(s_tok) & 0x7fffffffu;
 #pragma unroll
@@ -240,23 +286,19 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const EvictArgs a) {
     a.to_scale[which_lane][bh * to_blocks + (block_pos >> a.block_shift)] = s;
   if (lane < 16 && from >= 0) a.to_weights[bh * a.to_capacity + pos] = a.weights[bh * a.capacity + from];
   const float inv = kv8_inverse(s);
-  const int words = a.D >> 4;  // 16-byte pieces of a row
-  const int live = min(16, total - (base + warp * 16));
-#pragma unroll 1
+  const int live = total - (base + warp * 16);
+#pragma unroll
   for (int which = 0; which < 2; ++which) {
     const float si = __shfl_sync(0xffffffffu, inv, which * 16);
     const float sb = __shfl_sync(0xffffffffu, s, which * 16);
-    const uint8_t* src = a.codes[which] + bh * a.capacity * a.D;
-    uint8_t* dst = a.to_codes[which] + (bh * a.to_capacity + base + warp * 16) * a.D;
-    for (int i0 = 0; i0 < 16 * words; i0 += 32) {  // 16 * words is a multiple of 32: whole warps
-      const int i = i0 + lane;
-      const int t = i / words, c = i - t * words;
-      const int f = __shfl_sync(0xffffffffu, from, t);
+    uint4* dst = reinterpret_cast<uint4*>(a.to_codes[which] + (bh * a.to_capacity + base + warp * 16) * D);
+#pragma unroll
+    for (int i = 0; i < kIters; ++i) {
+      const int t = (i * 32 + lane) / kUnits;
       const float st = __shfl_sync(0xffffffffu, s_tok, which * 16 + t);
-      if (t >= live) continue;
-      uint4 v = *reinterpret_cast<const uint4*>(src + static_cast<int64_t>(f) * a.D + c * 16);
+      uint4 w = v[which][i];
       if (st != sb) {
-        uint32_t u[4] = {v.x, v.y, v.z, v.w};
+        uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           float x[4];
@@ -265,9 +307,9 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const EvictArgs a) {
           for (int d = 0; d < 4; ++d) x[d] = __fmul_rn(__fmul_rn(x[d], st), si);
           u[e] = sb < INFINITY ? Code::encode4(x[0], x[1], x[2], x[3]) : 0u;
         }
-        v = make_uint4(u[0], u[1], u[2], u[3]);
+        w = make_uint4(u[0], u[1], u[2], u[3]);
       }
-      *reinterpret_cast<uint4*>(dst + t * a.D + c * 16) = v;
+      if (t < live) dst[i * 32 + lane] = w;
     }
   }
 }

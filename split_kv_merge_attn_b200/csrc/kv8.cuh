@@ -50,8 +50,13 @@ struct Kv8Code {
       const float2 f0 = unpack2<__half>(h0), f1 = unpack2<__half>(h1);
       x[0] = f0.x; x[1] = f0.y; x[2] = f1.x; x[3] = f1.y;
     } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = static_cast<float>(static_cast<int8_t>(w >> (8 * e)));
+      // 0x4b000000 | u is 2^23 + u in fp32, with u = code + 128 (the type
+      // conversion instruction runs at an eighth of this rate)
+      const uint32_t u = w ^ 0x80808080u;
+      x[0] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440)) - 8388736.f;
+      x[1] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7441)) - 8388736.f;
+      x[2] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7442)) - 8388736.f;
+      x[3] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7443)) - 8388736.f;
     }
   }
 };
@@ -81,7 +86,8 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(const Kv8AppendArgs a) 
   // a programmatic dependent of the kernel before it: waits before any load
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int b = blockIdx.y / a.Hkv, h = blockIdx.y % a.Hkv, which = blockIdx.z;
+  // heads beside each other: in token-major rows they share DRAM pages
+  const int b = blockIdx.y, h = blockIdx.x % a.Hkv, which = blockIdx.z;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int start = min(max(a.start[b], 0), a.capacity);
   int count = a.S, first_row = 0;
@@ -93,14 +99,20 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(const Kv8AppendArgs a) 
     count = min(max(a.num_new[b], 0), a.S);
   }
   const int end = start + min(count, a.capacity - start);
-  const int base = (start / kKv8Window + static_cast<int>(blockIdx.x)) * kKv8Window;
+  const int base = (start / kKv8Window + static_cast<int>(blockIdx.x) / a.Hkv) * kKv8Window;
   if (base >= end || start >= end) return;  // the whole CTA: nothing new in this window
 
   const int cl = lane % kLanes, rl = lane / kLanes;
   const int pos0 = base + warp * 16 + rl;   // this lane's rows: pos0 + kRows * p
   const T* x = static_cast<const T*>(a.x[which]);
+  const int per = a.block >> 4;            // warps of one block
+  const int group = warp / per;
+  const int block_pos = base + group * a.block;
+  const bool touched = block_pos < end && block_pos + a.block > start;
+  const bool has_old = touched && block_pos < start;  // older tokens, with a scale of their own
+  uint8_t* codes = a.codes[which] + (static_cast<int64_t>(b) * a.Hkv + h) * a.capacity * static_cast<int64_t>(D) + cl * 8;
+  // a lane's rows: new values, or (first block only) the codes of older tokens
   uint4 v[kPasses];
-  uint32_t top = 0;  // largest magnitude bits, two 16-bit halves
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
     const int pos = pos0 + kRows * p;
@@ -112,25 +124,25 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(const Kv8AppendArgs a) 
       else if (a.token_major) row = (static_cast<int64_t>(b) * a.S + i) * a.Hkv + h;
       else row = (static_cast<int64_t>(b) * a.Hkv + h) * a.S + i;
       v[p] = __ldg(reinterpret_cast<const uint4*>(x + row * D + cl * 8));
+    } else if (has_old && pos < start) {
+      const uint2 w = *reinterpret_cast<const uint2*>(codes + static_cast<int64_t>(pos) * D);
+      v[p].x = w.x;
+      v[p].y = w.y;
     }
   }
+  uint32_t top = 0;  // largest magnitude bits of the new values, two 16-bit halves
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
     // magnitude bits of 16-bit floats order as whole numbers, NaN above infinity
-    top = __vmaxu2(top, __vmaxu2(__vmaxu2(v[p].x & 0x7fff7fffu, v[p].y & 0x7fff7fffu),
-                                 __vmaxu2(v[p].z & 0x7fff7fffu, v[p].w & 0x7fff7fffu)));
+    const uint32_t t = __vmaxu2(__vmaxu2(v[p].x & 0x7fff7fffu, v[p].y & 0x7fff7fffu),
+                                __vmaxu2(v[p].z & 0x7fff7fffu, v[p].w & 0x7fff7fffu));
+    if (pos0 + kRows * p >= start) top = __vmaxu2(top, t);
   }
   top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
 
   __shared__ uint32_t warp_top[8];
-  const int per = a.block >> 4;            // warps of one block
-  const int group = warp / per;
-  const int block_pos = base + group * a.block;
-  const bool touched = block_pos < end && block_pos + a.block > start;
   const int64_t at = (static_cast<int64_t>(b) * a.Hkv + h) * (a.capacity / a.block) + block_pos / a.block;
-  // a block that begins before `start` holds older tokens with a scale of their own
-  float s_old = 0.f;
-  if (touched && block_pos < start) s_old = a.scale[which][at];
+  const float s_old = has_old ? a.scale[which][at] : 0.f;
   if (lane == 0) warp_top[warp] = top;
   __syncthreads();  // also orders every read of the old scale before its new value is written
   if (!touched) return;
@@ -143,7 +155,6 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(const Kv8AppendArgs a) 
   const float inv = kv8_inverse(s);
   if (warp == group * per && lane == 0) a.scale[which][at] = s;
 
-  uint8_t* codes = a.codes[which] + (static_cast<int64_t>(b) * a.Hkv + h) * a.capacity * static_cast<int64_t>(D) + cl * 8;
   const bool wider = s > s_old || (poisoned && s_old < INFINITY);
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
@@ -160,13 +171,12 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(const Kv8AppendArgs a) 
     } else {
       if (!wider) continue;
       if (!poisoned) {
-        w = *dst;
         float c[4];
-        Code::decode4(w.x, c);
+        Code::decode4(v[p].x, c);
 #pragma unroll
         for (int e = 0; e < 4; ++e) c[e] = __fmul_rn(__fmul_rn(c[e], s_old), inv);
         w.x = Code::encode4(c[0], c[1], c[2], c[3]);
-        Code::decode4(w.y, c);
+        Code::decode4(v[p].y, c);
 #pragma unroll
         for (int e = 0; e < 4; ++e) c[e] = __fmul_rn(__fmul_rn(c[e], s_old), inv);
         w.y = Code::encode4(c[0], c[1], c[2], c[3]);
@@ -178,54 +188,65 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(const Kv8AppendArgs a) 
 
 // Fetch.  A window of the cache in 16 bits: out[b, h, i] = code * scale of
 // position start[b] + i, zero where that is not in [0, kv_len[b]).  Bound by
-// bytes (8 bits in, 16 out): one thread per 16 codes of K and of V.
+// bytes (8 bits in, 16 out).
 struct Kv8FetchArgs {
   const uint8_t* codes[2];
   const float* scale[2];
   void* out[2];
   const int32_t* start;    // [B] or null (= 0)
   const int32_t* kv_len;   // [B] or null (= capacity)
-  int B, Hkv, capacity, block, n, D;
+  int Hkv, capacity, block_shift, n;
   int token_major;         // out [B, n, Hkv, D] instead of [B, Hkv, n, D]
 };
 
-template <typename T, bool kE4M3>
+constexpr int kFetchUnroll = 4;  // 16-code pieces a thread has in flight
+
+template <int D, typename T, bool kE4M3>
 __global__ void __launch_bounds__(256) kv8_fetch_kernel(const Kv8FetchArgs a) {
+  constexpr int kUnits = D / 16;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int units = a.D >> 4;
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  const int64_t row = id / units;             // (b, h, i)
-  const int u = static_cast<int>(id - row * units);
-  if (row >= static_cast<int64_t>(a.B) * a.Hkv * a.n) return;
-  const int64_t bh = row / a.n;
-  const int i = static_cast<int>(row - bh * a.n);
-  const int b = static_cast<int>(bh / a.Hkv), h = static_cast<int>(bh - static_cast<int64_t>(b) * a.Hkv);
-  const int64_t pos = static_cast<int64_t>(a.start != nullptr ? a.start[b] : 0) + i;
+  const int bh = blockIdx.y, which = blockIdx.z;
+  const int b = bh / a.Hkv, h = bh - b * a.Hkv;
+  const int64_t start = a.start != nullptr ? a.start[b] : 0;
   const int len = a.kv_len != nullptr ? min(a.kv_len[b], a.capacity) : a.capacity;
-  const int which = blockIdx.y;
-  uint4 o0 = make_uint4(0, 0, 0, 0), o1 = o0;
-  if (pos >= 0 && pos < len) {
-    const float s = a.scale[which][bh * (a.capacity / a.block) + pos / a.block];
-    const uint4 w = *reinterpret_cast<const uint4*>(a.codes[which] + (bh * a.capacity + pos) * a.D + u * 16);
-    float x[4];
-    Kv8Code<kE4M3>::decode4(w.x, x);
-    o0.x = pack2<T>(x[0] * s, x[1] * s);
-    o0.y = pack2<T>(x[2] * s, x[3] * s);
-    Kv8Code<kE4M3>::decode4(w.y, x);
-    o0.z = pack2<T>(x[0] * s, x[1] * s);
-    o0.w = pack2<T>(x[2] * s, x[3] * s);
-    Kv8Code<kE4M3>::decode4(w.z, x);
-    o1.x = pack2<T>(x[0] * s, x[1] * s);
-    o1.y = pack2<T>(x[2] * s, x[3] * s);
-    Kv8Code<kE4M3>::decode4(w.w, x);
-    o1.z = pack2<T>(x[0] * s, x[1] * s);
-    o1.w = pack2<T>(x[2] * s, x[3] * s);
+  const uint8_t* codes = a.codes[which] + static_cast<int64_t>(bh) * a.capacity * D;
+  const float* scale = a.scale[which] + static_cast<int64_t>(bh) * (a.capacity >> a.block_shift);
+  T* out = static_cast<T*>(a.out[which]);
+  constexpr int kRowsCta = 256 * kFetchUnroll / kUnits;
+  const int i0 = blockIdx.x * kRowsCta + threadIdx.x / kUnits, u = threadIdx.x % kUnits;
+  uint4 w[kFetchUnroll];
+  float s[kFetchUnroll];
+#pragma unroll
+  for (int j = 0; j < kFetchUnroll; ++j) {
+    const int i = i0 + j * (256 / kUnits);
+    const int64_t pos = start + i;
+    w[j] = make_uint4(0, 0, 0, 0);
+    s[j] = 0.f;  // a position without a token: zeros (e4m3 and, below, int8 codes 0)
+    if (i < a.n && pos >= 0 && pos < len) {
+      w[j] = __ldg(reinterpret_cast<const uint4*>(codes + pos * D) + u);
+      s[j] = __ldg(scale + (pos >> a.block_shift));
+    }
   }
-  const int64_t orow = a.token_major ? (static_cast<int64_t>(b) * a.n + i) * a.Hkv + h : row;
-  uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out[which]) + orow * a.D + u * 16);
-  dst[0] = o0;
-  dst[1] = o1;
+#pragma unroll
+  for (int j = 0; j < kFetchUnroll; ++j) {
+    const int i = i0 + j * (256 / kUnits);
+    if (i >= a.n) break;
+    const uint32_t in[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+    uint32_t o[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float x[4];
+      Kv8Code<kE4M3>::decode4(in[e], x);
+      o[2 * e] = pack2<T>(x[0] * s[j], x[1] * s[j]);
+      o[2 * e + 1] = pack2<T>(x[2] * s[j], x[3] * s[j]);
+    }
+    const int64_t row = a.token_major ? (static_cast<int64_t>(b) * a.n + i) * a.Hkv + h
+                                      : static_cast<int64_t>(bh) * a.n + i;
+    uint4* dst = reinterpret_cast<uint4*>(out + row * D) + 2 * u;
+    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  }
 }
 
 }  // namespace skv

@@ -109,6 +109,27 @@ int launch_append_d(const Kv8AppendArgs& a, int D, skv_code codes, dim3 grid, sk
   return launch_append<256, T>(a, codes, grid, st);
 }
 
+template <int D, typename T>
+int launch_fetch(const Kv8FetchArgs& a, int B, skv_code codes, skv_stream_t st) {
+  const dim3 grid(static_cast<unsigned>(ceil_div64(a.n, 256 * kFetchUnroll / (D / 16))),
+                  static_cast<unsigned>(B * a.Hkv), 2);
+  return codes == SKV_E4M3 ? launch(kv8_fetch_kernel<D, T, true>, grid, 256, 0, st, 1, a)
+                           : launch(kv8_fetch_kernel<D, T, false>, grid, 256, 0, st, 1, a);
+}
+
+template <typename T>
+int launch_fetch_d(const Kv8FetchArgs& a, int B, int D, skv_code codes, skv_stream_t st) {
+  if (D == 64) return launch_fetch<64, T>(a, B, codes, st);
+  if (D == 128) return launch_fetch<128, T>(a, B, codes, st);
+  return launch_fetch<256, T>(a, B, codes, st);
+}
+
+template <int D>
+int launch_move(const EvictArgs& a, dim3 grid, skv_code codes, skv_stream_t st) {
+  return codes == SKV_E4M3 ? launch(evict_move_kernel<D, true>, grid, 256, 0, st, 1, a)
+                           : launch(evict_move_kernel<D, false>, grid, 256, 0, st, 1, a);
+}
+
 // ---- tile maps: the codes as rows of 128 (D = 64: two tokens; D = 128: one)
 // or 256 bytes, boxes 128 bytes wide, 128-byte swizzle
 int encode_codes(CUtensorMap* m, const void* base, int64_t tokens, int D) {
@@ -232,7 +253,8 @@ skv_status rope_apply(const void* q, const void* k, void* q_out, void* k_out, co
   if (!std::isfinite(factor)) return SKV_ERR_INVALID_ARG;
   if ((interleaved != 0 && interleaved != 1) || (inverse != 0 && inverse != 1)) return SKV_ERR_INVALID_ARG;
   if (skv_status s = check_half(dtype)) return s;
-  if (D % 16 != 0 || rotary_dim % 16 != 0) return SKV_ERR_UNSUPPORTED;
+  // (the table of a CTA holds one token's pairs)
+  if (D % 16 != 0 || rotary_dim % 16 != 0 || rotary_dim > kRopeTableBytes / 4) return SKV_ERR_UNSUPPORTED;
   const size_t row = static_cast<size_t>(B) * S * D * 2;
   const size_t nq = row * Hq, nk = row * Hkv;
   // in place is fine, any other overlap is not
@@ -258,20 +280,24 @@ skv_status rope_apply(const void* q, const void* k, void* q_out, void* k_out, co
   a.token_major = layout != SKV_HND;
   const int sms = sm_count();
   if (sms <= 0) return cuda_status(cudaErrorNoDevice);
-  const int64_t threads = static_cast<int64_t>(B) * S * (D / 16);
+  const int64_t tokens = static_cast<int64_t>(B) * S;
   const int64_t heads = static_cast<int64_t>(a.heads[0]) + a.heads[1];
-  const int64_t group = std::min<int64_t>(8, std::max<int64_t>(1, heads * threads / (static_cast<int64_t>(sms) * 1024)));
-  a.group = static_cast<int>(group);
-  const int64_t gx = ceil_div64(threads, 256), gy = ceil_div64(heads, group);
-  if (gx > 0x7fffffff || gy > 65535) return SKV_ERR_UNSUPPORTED;
+  // Eight tokens a CTA and all heads where that gives every SM two CTAs (fewer
+  // tokens where their table would not fit); else one token and as many heads as
+  // give every thread one unit.
+  const int fit = std::max(1, kRopeTableBytes / 4 / rotary_dim);
+  a.tokens = tokens >= static_cast<int64_t>(sms) * 16 ? std::min(8, fit) : 1;
+  a.group = static_cast<int>(a.tokens > 1 ? heads : std::min<int64_t>(heads, std::max(1, kRopeThreads * 16 / D)));
+  const int64_t gx = ceil_div64(tokens, a.tokens), gy = ceil_div64(heads, a.group);
+  if (gx > 0x7fffffff || gy > 65535 || heads * a.tokens * (D / 16) > (1 << 30)) return SKV_ERR_UNSUPPORTED;
   const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy));
   int e;
   if (dtype == SKV_BF16)
-    e = interleaved ? launch(rope_kernel<__nv_bfloat16, true>, grid, 256, 0, stream, 1, a)
-                    : launch(rope_kernel<__nv_bfloat16, false>, grid, 256, 0, stream, 1, a);
+    e = interleaved ? launch(rope_kernel<__nv_bfloat16, true>, grid, kRopeThreads, 0, stream, 1, a)
+                    : launch(rope_kernel<__nv_bfloat16, false>, grid, kRopeThreads, 0, stream, 1, a);
   else
-    e = interleaved ? launch(rope_kernel<__half, true>, grid, 256, 0, stream, 1, a)
-                    : launch(rope_kernel<__half, false>, grid, 256, 0, stream, 1, a);
+    e = interleaved ? launch(rope_kernel<__half, true>, grid, kRopeThreads, 0, stream, 1, a)
+                    : launch(rope_kernel<__half, false>, grid, kRopeThreads, 0, stream, 1, a);
   return cuda_status(e);
 }
 
@@ -310,7 +336,8 @@ skv_status kv8_append(const void* k_new, const void* v_new, void* k_codes, void*
   // windows that S tokens touch at most, wherever they start
   const int64_t windows = std::min<int64_t>((static_cast<int64_t>(S) + kKv8Window - 2) / kKv8Window + 1,
                                             ceil_div64(capacity, kKv8Window));
-  const dim3 grid(static_cast<unsigned>(windows), static_cast<unsigned>(B * Hkv), 2);
+  if (windows * Hkv > 0x7fffffff) return SKV_ERR_UNSUPPORTED;
+  const dim3 grid(static_cast<unsigned>(windows * Hkv), static_cast<unsigned>(B), 2);
   return cuda_status(dtype == SKV_BF16 ? launch_append_d<__nv_bfloat16>(a, D, codes, grid, stream)
                                        : launch_append_d<__half>(a, D, codes, grid, stream));
 }
@@ -333,25 +360,13 @@ skv_status kv8_fetch(const void* k_codes, const void* v_codes, const float* k_sc
   a.out[1] = v_out;
   a.start = start;
   a.kv_len = kv_len;
-  a.B = B;
   a.Hkv = Hkv;
   a.capacity = capacity;
-  a.block = block;
+  a.block_shift = log2_of(block);
   a.n = n;
-  a.D = D;
   a.token_major = layout == SKV_NHD;
-  const int64_t blocks = ceil_div64(static_cast<int64_t>(B) * Hkv * n * (D / 16), 256);
-  if (blocks > 0x7fffffff) return SKV_ERR_UNSUPPORTED;
-  const dim3 grid(static_cast<unsigned>(blocks), 2);
-  const bool e4 = codes == SKV_E4M3;
-  int e;
-  if (dtype == SKV_BF16)
-    e = e4 ? launch(kv8_fetch_kernel<__nv_bfloat16, true>, grid, 256, 0, stream, 1, a)
-           : launch(kv8_fetch_kernel<__nv_bfloat16, false>, grid, 256, 0, stream, 1, a);
-  else
-    e = e4 ? launch(kv8_fetch_kernel<__half, true>, grid, 256, 0, stream, 1, a)
-           : launch(kv8_fetch_kernel<__half, false>, grid, 256, 0, stream, 1, a);
-  return cuda_status(e);
+  return cuda_status(dtype == SKV_BF16 ? launch_fetch_d<__nv_bfloat16>(a, B, D, codes, stream)
+                                       : launch_fetch_d<__half>(a, B, D, codes, stream));
 }
 
 // ------------------------------------------------------------------ decode
@@ -512,7 +527,6 @@ skv_status kv8_evict(const void* k_codes, const void* v_codes, const float* k_sc
   a.to_weights = to_weights;
   a.B = B;
   a.Hkv = Hkv;
-  a.D = D;
   a.capacity = capacity;
   a.to_capacity = to_capacity;
   a.block_shift = log2_of(block);
@@ -526,8 +540,8 @@ skv_status kv8_evict(const void* k_codes, const void* v_codes, const float* k_sc
   if (e) return cuda_status(e);
   const int64_t most = std::min(budget, capacity);
   const dim3 grid(static_cast<unsigned>(ceil_div64(most, kKv8Window)), static_cast<unsigned>(B * Hkv));
-  e = codes == SKV_E4M3 ? launch(evict_move_kernel<true>, grid, 256, 0, stream, 1, a)
-                        : launch(evict_move_kernel<false>, grid, 256, 0, stream, 1, a);
+  e = D == 64 ? launch_move<64>(a, grid, codes, stream)
+              : (D == 128 ? launch_move<128>(a, grid, codes, stream) : launch_move<256>(a, grid, codes, stream));
   return cuda_status(e);
 }
 
