@@ -289,7 +289,8 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const EvictArgs a) {
   const int live = total - (base + warp * 16);
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
-    const float si = __shfl_sync(0xffffffffu, inv, which * 16);
+    const float i1 = __shfl_sync(0xffffffffu, inv, which * 16);
+    const uint64_t si = f2_pack(i1, i1);
     const float sb = __shfl_sync(0xffffffffu, s, which * 16);
     uint4* dst = reinterpret_cast<uint4*>(a.to_codes[which] + (bh * a.to_capacity + base + warp * 16) * D);
 #pragma unroll
@@ -298,16 +299,11 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const EvictArgs a) {
       const float st = __shfl_sync(0xffffffffu, s_tok, which * 16 + t);
       uint4 w = v[which][i];
       if (st != sb) {
-        uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x[4];
-          Code::decode4(u[e], x);
-#pragma unroll
-          for (int d = 0; d < 4; ++d) x[d] = __fmul_rn(__fmul_rn(x[d], st), si);
-          u[e] = sb < INFINITY ? Code::encode4(x[0], x[1], x[2], x[3]) : 0u;
-        }
-        w = make_uint4(u[0], u[1], u[2], u[3]);
+        const bool good = sb < INFINITY;
+        w.x = good ? Code::recode4(w.x, st, si) : 0u;
+        w.y = good ? Code::recode4(w.y, st, si) : 0u;
+        w.z = good ? Code::recode4(w.z, st, si) : 0u;
+        w.w = good ? Code::recode4(w.w, st, si) : 0u;
       }
       if (t < live) dst[i * 32 + lane] = w;
     }

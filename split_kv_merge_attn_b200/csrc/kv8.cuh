@@ -27,19 +27,24 @@ constexpr float kKv8TinyScale = 1.17549435e-38f;  // 2^-126
 template <bool kE4M3>
 struct Kv8Code {
   static constexpr float kMax = kE4M3 ? 448.f : 127.f;
-  // four values already multiplied by 1 / scale (|.| <= kMax up to rounding)
-  static __device__ __forceinline__ uint32_t encode4(float x0, float x1, float x2, float x3) {
+  // codes of four values times inv = 1 / scale (|.| <= kMax up to rounding)
+  static __device__ __forceinline__ uint32_t encode4(float2 a, float2 b, uint64_t inv) {
+    const uint64_t p = fmul2(f2_pack(a.x, a.y), inv), q = fmul2(f2_pack(b.x, b.y), inv);
     if constexpr (kE4M3) {
+      const float2 x = f2_unpack(p), y = f2_unpack(q);
       uint16_t lo, hi;
-      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x1), "f"(x0));
-      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x3), "f"(x2));
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x.y), "f"(x.x));
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(y.y), "f"(y.x));
       return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
     } else {
       // adding 1.5 * 2^23 rounds to a whole number (ties to even) in the low
       // bits; the low byte is the two's complement code
-      const uint32_t a = __float_as_uint(__fadd_rn(x0, 12582912.f)), b = __float_as_uint(__fadd_rn(x1, 12582912.f));
-      const uint32_t c = __float_as_uint(__fadd_rn(x2, 12582912.f)), d = __float_as_uint(__fadd_rn(x3, 12582912.f));
-      return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+      // (scalar sums: a packed product and a packed sum were contracted into one
+      // rounding, which is another code where a product lies next to a tie)
+      const float2 x = f2_unpack(p), y = f2_unpack(q);
+      const uint32_t i0 = __float_as_uint(__fadd_rn(x.x, 12582912.f)), i1 = __float_as_uint(__fadd_rn(x.y, 12582912.f));
+      const uint32_t i2 = __float_as_uint(__fadd_rn(y.x, 12582912.f)), i3 = __float_as_uint(__fadd_rn(y.y, 12582912.f));
+      return __byte_perm(__byte_perm(i0, i1, 0x0040), __byte_perm(i2, i3, 0x0040), 0x5410);
     }
   }
   static __device__ __forceinline__ void decode4(uint32_t w, float (&x)[4]) {
@@ -58,6 +63,13 @@ struct Kv8Code {
       x[2] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7442)) - 8388736.f;
       x[3] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7443)) - 8388736.f;
     }
+  }
+  // codes of (code * from) / to, given 1 / to
+  static __device__ __forceinline__ uint32_t recode4(uint32_t w, float from, uint64_t inv) {
+    float x[4];
+    decode4(w, x);
+    return encode4(make_float2(__fmul_rn(x[0], from), __fmul_rn(x[1], from)),
+                   make_float2(__fmul_rn(x[2], from), __fmul_rn(x[3], from)), inv);
   }
 };
 
@@ -78,7 +90,7 @@ struct Kv8AppendArgs {
 };
 
 template <int D, typename T, bool kE4M3>
-__global__ void __launch_bounds__(256) kv8_append_kernel(const Kv8AppendArgs a) {
+__global__ void __launch_bounds__(256, D == 64 ? 5 : (D == 128 ? 4 : 2)) kv8_append_kernel(const Kv8AppendArgs a) {
   using Code = Kv8Code<kE4M3>;
   constexpr int kLanes = D / 8;            // lanes of one row, 8 values each
   constexpr int kRows = 32 / kLanes;       // rows a warp takes at once
@@ -103,40 +115,48 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(const Kv8AppendArgs a) 
   if (base >= end || start >= end) return;  // the whole CTA: nothing new in this window
 
   const int cl = lane % kLanes, rl = lane / kLanes;
-  const int pos0 = base + warp * 16 + rl;   // this lane's rows: pos0 + kRows * p
-  const T* x = static_cast<const T*>(a.x[which]);
+  const int wpos = base + warp * 16;       // this warp's first position
+  const int pos0 = wpos + rl;              // this lane's rows: pos0 + kRows * p
   const int per = a.block >> 4;            // warps of one block
   const int group = warp / per;
   const int block_pos = base + group * a.block;
   const bool touched = block_pos < end && block_pos + a.block > start;
   const bool has_old = touched && block_pos < start;  // older tokens, with a scale of their own
-  uint8_t* codes = a.codes[which] + (static_cast<int64_t>(b) * a.Hkv + h) * a.capacity * static_cast<int64_t>(D) + cl * 8;
+  const bool whole = wpos >= start && wpos + 16 <= end;  // new rows only
+  // rows of token i: row0 + i * step
+  const int64_t step = (a.cu != nullptr || a.token_major) ? a.Hkv : 1;
+  const int64_t row0 = a.cu != nullptr ? static_cast<int64_t>(first_row) * a.Hkv + h
+                       : a.token_major ? static_cast<int64_t>(b) * a.S * a.Hkv + h
+                                       : (static_cast<int64_t>(b) * a.Hkv + h) * a.S;
+  const T* src = static_cast<const T*>(a.x[which]) + (row0 + (pos0 - start) * step) * D + cl * 8;
+  const int64_t src_pass = step * kRows * D;
+  uint8_t* codes = a.codes[which] + ((static_cast<int64_t>(b) * a.Hkv + h) * a.capacity + pos0) * D + cl * 8;
   // a lane's rows: new values, or (first block only) the codes of older tokens
   uint4 v[kPasses];
+  uint32_t top = 0;  // largest magnitude bits of the new values, two 16-bit halves
+  if (whole) {
 #pragma unroll
-  for (int p = 0; p < kPasses; ++p) {
-    const int pos = pos0 + kRows * p;
-    v[p] = make_uint4(0, 0, 0, 0);
-    if (pos >= start && pos < end) {
-      int64_t row;
-      const int i = pos - start;
-      if (a.cu != nullptr) row = (static_cast<int64_t>(first_row) + i) * a.Hkv + h;
-      else if (a.token_major) row = (static_cast<int64_t>(b) * a.S + i) * a.Hkv + h;
-      else row = (static_cast<int64_t>(b) * a.Hkv + h) * a.S + i;
-      v[p] = __ldg(reinterpret_cast<const uint4*>(x + row * D + cl * 8));
-    } else if (has_old && pos < start) {
-      const uint2 w = *reinterpret_cast<const uint2*>(codes + static_cast<int64_t>(pos) * D);
-      v[p].x = w.x;
-      v[p].y = w.y;
+    for (int p = 0; p < kPasses; ++p) v[p] = __ldg(reinterpret_cast<const uint4*>(src + p * src_pass));
+  } else {
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+      const int pos = pos0 + kRows * p;
+      v[p] = make_uint4(0, 0, 0, 0);
+      if (pos >= start && pos < end) {
+        v[p] = __ldg(reinterpret_cast<const uint4*>(src + p * src_pass));
+      } else if (has_old && pos < start) {
+        const uint2 w = *reinterpret_cast<const uint2*>(codes + kRows * p * D);
+        v[p].x = w.x;
+        v[p].y = w.y;
+      }
     }
   }
-  uint32_t top = 0;  // largest magnitude bits of the new values, two 16-bit halves
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
     // magnitude bits of 16-bit floats order as whole numbers, NaN above infinity
     const uint32_t t = __vmaxu2(__vmaxu2(v[p].x & 0x7fff7fffu, v[p].y & 0x7fff7fffu),
                                 __vmaxu2(v[p].z & 0x7fff7fffu, v[p].w & 0x7fff7fffu));
-    if (pos0 + kRows * p >= start) top = __vmaxu2(top, t);
+    if (whole || pos0 + kRows * p >= start) top = __vmaxu2(top, t);
   }
   top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
 
@@ -155,34 +175,28 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(const Kv8AppendArgs a) 
   const float inv = kv8_inverse(s);
   if (warp == group * per && lane == 0) a.scale[which][at] = s;
 
+  const uint64_t inv2 = f2_pack(inv, inv);
+  auto encode = [&](const uint4& x) {
+    uint2 w;
+    w.x = Code::encode4(unpack2<T>(x.x), unpack2<T>(x.y), inv2);
+    w.y = Code::encode4(unpack2<T>(x.z), unpack2<T>(x.w), inv2);
+    return w;
+  };
+  if (whole && !poisoned) {
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) *reinterpret_cast<uint2*>(codes + kRows * p * D) = encode(v[p]);
+    return;
+  }
   const bool wider = s > s_old || (poisoned && s_old < INFINITY);
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
     const int pos = pos0 + kRows * p;
-    if (pos >= end) continue;
-    uint2* dst = reinterpret_cast<uint2*>(codes + static_cast<int64_t>(pos) * D);
+    if (pos >= end || (pos < start && !wider)) continue;
     uint2 w = make_uint2(0, 0);
-    if (pos >= start) {
-      if (!poisoned) {
-        const float2 f0 = unpack2<T>(v[p].x), f1 = unpack2<T>(v[p].y), f2 = unpack2<T>(v[p].z), f3 = unpack2<T>(v[p].w);
-        w.x = Code::encode4(__fmul_rn(f0.x, inv), __fmul_rn(f0.y, inv), __fmul_rn(f1.x, inv), __fmul_rn(f1.y, inv));
-        w.y = Code::encode4(__fmul_rn(f2.x, inv), __fmul_rn(f2.y, inv), __fmul_rn(f3.x, inv), __fmul_rn(f3.y, inv));
-      }
-    } else {
-      if (!wider) continue;
-      if (!poisoned) {
-        float c[4];
-        Code::decode4(v[p].x, c);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) c[e] = __fmul_rn(__fmul_rn(c[e], s_old), inv);
-        w.x = Code::encode4(c[0], c[1], c[2], c[3]);
-        Code::decode4(v[p].y, c);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) c[e] = __fmul_rn(__fmul_rn(c[e], s_old), inv);
-        w.y = Code::encode4(c[0], c[1], c[2], c[3]);
-      }
-    }
-    *dst = w;
+    if (!poisoned)
+      w = pos >= start ? encode(v[p])
+                       : make_uint2(Code::recode4(v[p].x, s_old, inv2), Code::recode4(v[p].y, s_old, inv2));
+    *reinterpret_cast<uint2*>(codes + kRows * p * D) = w;
   }
 }
 

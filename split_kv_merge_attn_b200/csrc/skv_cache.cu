@@ -253,8 +253,9 @@ skv_status rope_apply(const void* q, const void* k, void* q_out, void* k_out, co
   if (!std::isfinite(factor)) return SKV_ERR_INVALID_ARG;
   if ((interleaved != 0 && interleaved != 1) || (inverse != 0 && inverse != 1)) return SKV_ERR_INVALID_ARG;
   if (skv_status s = check_half(dtype)) return s;
-  // (the table of a CTA holds one token's pairs)
-  if (D % 16 != 0 || rotary_dim % 16 != 0 || rotary_dim > kRopeTableBytes / 4) return SKV_ERR_UNSUPPORTED;
+  // a CTA's table holds a token's pairs, and its threads a head's units
+  if (D % 16 != 0 || rotary_dim % 16 != 0 || rotary_dim * 4 > kRopeTableBytes || D > 16 * kRopeMaxThreads)
+    return SKV_ERR_UNSUPPORTED;
   const size_t row = static_cast<size_t>(B) * S * D * 2;
   const size_t nq = row * Hq, nk = row * Hkv;
   // in place is fine, any other overlap is not
@@ -273,7 +274,6 @@ skv_status rope_apply(const void* q, const void* k, void* q_out, void* k_out, co
   a.inv_freq = inv_freq;
   a.factor = factor;
   a.inverse = inverse;
-  a.B = B;
   a.S = S;
   a.D = D;
   a.R = rotary_dim;
@@ -281,23 +281,28 @@ skv_status rope_apply(const void* q, const void* k, void* q_out, void* k_out, co
   const int sms = sm_count();
   if (sms <= 0) return cuda_status(cudaErrorNoDevice);
   const int64_t tokens = static_cast<int64_t>(B) * S;
+  if (tokens > (1 << 30)) return SKV_ERR_UNSUPPORTED;
   const int64_t heads = static_cast<int64_t>(a.heads[0]) + a.heads[1];
-  // Eight tokens a CTA and all heads where that gives every SM two CTAs (fewer
-  // tokens where their table would not fit); else one token and as many heads as
-  // give every thread one unit.
-  const int fit = std::max(1, kRopeTableBytes / 4 / rotary_dim);
-  a.tokens = tokens >= static_cast<int64_t>(sms) * 16 ? std::min(8, fit) : 1;
-  a.group = static_cast<int>(a.tokens > 1 ? heads : std::min<int64_t>(heads, std::max(1, kRopeThreads * 16 / D)));
-  const int64_t gx = ceil_div64(tokens, a.tokens), gy = ceil_div64(heads, a.group);
-  if (gx > 0x7fffffff || gy > 65535 || heads * a.tokens * (D / 16) > (1 << 30)) return SKV_ERR_UNSUPPORTED;
-  const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy));
+  // all tokens of a CTA at once where that still gives every SM two CTAs and their
+  // table fits, else one; the heads in equal groups of at most 512 threads
+  a.tokens = static_cast<int>(tokens);
+  a.per_cta = tokens >= static_cast<int64_t>(sms) * 2 * kRopeTokens && rotary_dim * 4 * kRopeTokens <= kRopeTableBytes
+                  ? kRopeTokens : 1;
+  const int units = D / 16;
+  const int64_t gx = ceil_div64(tokens, a.per_cta), gy = ceil_div64(heads * units, kRopeMaxThreads);
+  a.group = static_cast<int>(ceil_div64(heads, gy));
+  while (a.group > 1 && a.group * units > kRopeMaxThreads) --a.group;
+  const int threads = static_cast<int>(ceil_div64(static_cast<int64_t>(a.group) * units, 32) * 32);
+  const int64_t groups = ceil_div64(heads, a.group);
+  if (groups > 65535) return SKV_ERR_UNSUPPORTED;
+  const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(groups));
   int e;
   if (dtype == SKV_BF16)
-    e = interleaved ? launch(rope_kernel<__nv_bfloat16, true>, grid, kRopeThreads, 0, stream, 1, a)
-                    : launch(rope_kernel<__nv_bfloat16, false>, grid, kRopeThreads, 0, stream, 1, a);
+    e = interleaved ? launch(rope_kernel<__nv_bfloat16, true>, grid, threads, 0, stream, 1, a)
+                    : launch(rope_kernel<__nv_bfloat16, false>, grid, threads, 0, stream, 1, a);
   else
-    e = interleaved ? launch(rope_kernel<__half, true>, grid, kRopeThreads, 0, stream, 1, a)
-                    : launch(rope_kernel<__half, false>, grid, kRopeThreads, 0, stream, 1, a);
+    e = interleaved ? launch(rope_kernel<__half, true>, grid, threads, 0, stream, 1, a)
+                    : launch(rope_kernel<__half, false>, grid, threads, 0, stream, 1, a);
   return cuda_status(e);
 }
 
