@@ -1,8 +1,10 @@
 """Python binding of ``libsplitkv.so`` (the C ABI declared in include/splitkv.h).
 
 Argument marshalling only: shapes are read off the tensors, device pointers
-and the current CUDA stream are passed through ctypes, and every step of the
-computation runs in the library's sm_100a kernels.  PyTorch supplies device
+and the current CUDA stream are passed through ctypes (the short calls around
+the 8-bit cache: through a small extension module, whose checks take less time
+than their kernels), and every step of the computation runs in the library's
+sm_100a kernels.  PyTorch supplies device
 memory (outputs and workspace are allocated with ``torch.empty`` when the
 caller does not pass them) and streams.  There is no fallback: if the shared
 library is missing or a call fails, an exception is raised.
@@ -24,11 +26,13 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.util
 import os
 from typing import NamedTuple, Optional, Sequence, Tuple
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libsplitkv.so")
+TORCH_LIB_PATH = os.path.join(HERE, "_skv_torch.so")
 
 SKV_OK, SKV_ERR_INVALID_ARG, SKV_ERR_UNSUPPORTED, SKV_ERR_WORKSPACE_TOO_SMALL, SKV_ERR_CUDA = range(5)
 DTYPES = {"bf16": 0, "fp16": 1, "fp32": 2}
@@ -192,63 +196,33 @@ def _workspace(nbytes: int, device, workspace):
     return workspace, workspace.numel() * workspace.element_size()
 
 
-class _Runtime:
-    """What the short-call wrappers need of PyTorch, looked up once."""
-
-    def __init__(self):
-        torch = _torch()
-        self.torch = torch
-        self.int32, self.float32, self.float64 = torch.int32, torch.float32, torch.float64
-        self.half = {torch.bfloat16: 0, torch.float16: 1}
-        self.codes = {torch.int8: 0, torch.float8_e4m3fn: 1}
-        self.empty, self.empty_like = torch.empty, torch.empty_like
-        self.current_device = torch.cuda.current_device
-        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-            lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+# The library's functions that _skv_torch calls, in the order its bind() takes them.
+_TORCH_FUNCTIONS = ("rope_apply", "kv8_append", "kv8_fetch", "attn_splitkv_kv8_plan", "attn_splitkv_kv8_workspace",
+                    "attn_splitkv_decode_kv8", "kv8_evict")
 
 
 @functools.lru_cache(maxsize=None)
-def _runtime() -> _Runtime:
-    return _Runtime()
+def _torch_calls():
+    """The extension module that marshals the short calls (csrc/skv_torch.cpp), loaded on first use."""
+    _torch()
+    if not os.path.exists(TORCH_LIB_PATH):
+        raise RuntimeError(f"{TORCH_LIB_PATH} is missing: build it with `python -m split_kv_merge_attn_b200._build`")
+    spec = importlib.util.spec_from_file_location("split_kv_merge_attn_b200._skv_torch", TORCH_LIB_PATH)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    m.bind(SkvError, *(ctypes.cast(getattr(lib(), f), ctypes.c_void_p).value for f in _TORCH_FUNCTIONS))
+    return m
 
 
-def _refuse(name, t, shape, dtype, dev) -> None:
-    """Says what is wrong with a tensor that _arg did not take."""
-    _expect(t is not None, f"{name} is needed")
-    _expect(t.dtype == dtype, f"{name} has dtype {t.dtype}, expected {dtype}")
-    _expect(tuple(t.shape) == tuple(shape), f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    _need_cuda(t)
-    raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
-
-
-def _arg(name, t, shape, dtype, dev) -> int:
-    """The address of a tensor of exactly this shape, type and device, contiguous."""
-    if t is None or t.dtype != dtype or t.shape != shape or t.get_device() != dev or dev < 0 or not t.is_contiguous():
-        _refuse(name, t, shape, dtype, dev)
-    return t.data_ptr()
-
-
-def _opt(name, t, shape, dtype, dev) -> Optional[int]:
-    return None if t is None else _arg(name, t, shape, dtype, dev)
-
-
-def _half(rt, dtype, name: str) -> int:
-    code = rt.half.get(dtype)
-    _expect(code is not None, f"{name} must be bfloat16 or float16" if code is None else "")
+def _layout(layout: str) -> int:
+    code = LAYOUTS.get(layout)
+    if code is None:
+        raise ValueError(f"unknown layout {layout!r}")
     return code
 
 
-def _call(rt, what: str, dev: int, stream, *args) -> None:
-    """Calls the library with `dev` current and the stream as the last argument."""
-    fn = getattr(lib(), what)
-    s = rt.raw_stream(dev) if stream is None else stream.cuda_stream
-    if rt.current_device() == dev:
-        st = fn(*args, s)
-    else:
-        with rt.torch.cuda.device(dev):
-            st = fn(*args, s)
-    if st != SKV_OK:
-        raise SkvError(st, what)
+def _handle(stream) -> Optional[int]:
+    return None if stream is None else stream.cuda_stream
 
 
 # ------------------------------------------------------------------ queries
@@ -630,37 +604,8 @@ def rope_apply(q, k, positions, inv_freq, layout: str = "HND", interleaved: bool
     (2i, 2i+1) instead of (i, i + R/2).  inverse: the transpose, i.e. the
     gradient of the inputs given that of the outputs.  q_out=q, k_out=k work in
     place.  Returns (q_out, k_out)."""
-    rt = _runtime()
-    if layout not in LAYOUTS or q.dim() != (3 if layout == "TND" else 4):
-        raise ValueError(f"unknown layout {layout!r}, or q has not its dimensions ({q.dim()})")
-    shape, dt, dev = q.shape, q.dtype, q.get_device()
-    if layout == "HND":
-        B, Hq, S, D = shape
-    elif layout == "NHD":
-        B, S, Hq, D = shape
-    else:
-        B, (S, Hq, D) = 1, shape
-    code = _half(rt, dt, "q")
-    pq = _arg("q", q, shape, dt, dev)
-    pk, Hkv = None, 0
-    if k is not None:
-        Hkv = k.shape[2 if layout == "NHD" else 1] if k.dim() == q.dim() else 0
-        k_shape = (B, Hkv, S, D) if layout == "HND" else ((B, S, Hkv, D) if layout == "NHD" else (S, Hkv, D))
-        pk = _arg("k", k, k_shape, dt, dev)
-    elif k_out is not None:
-        raise ValueError("k_out without k")
-    pp = _arg("positions", positions, (S,) if layout == "TND" else (B, S), rt.int32, dev)
-    pf = _arg("inv_freq", inv_freq, (inv_freq.numel(),), rt.float64, dev)
-    if q_out is None:
-        q_out = rt.empty_like(q)
-    if k_out is None and k is not None:
-        k_out = rt.empty_like(k)
-    pqo = _arg("q_out", q_out, shape, dt, dev)
-    pko = None if k is None else _arg("k_out", k_out, k_shape, dt, dev)
-    if S and B:
-        _call(rt, "rope_apply", dev, stream, pq, pk, pqo, pko, pp, pf, B, Hq, Hkv, S, D, 2 * inv_freq.numel(),
-              float(factor), code, LAYOUTS[layout], 1 if interleaved else 0, 1 if inverse else 0)
-    return q_out, k_out
+    return _torch_calls().rope_apply(q, k, positions, inv_freq, _layout(layout), interleaved, factor, inverse, q_out, k_out,
+                                     _handle(stream))
 
 
 # ------------------------------------------------------------------ 8-bit cache
@@ -687,20 +632,6 @@ def kv8_cache(B: int, Hkv: int, capacity: int, D: int, block: int = 64, codes: s
     return KV8Cache(*code, *scale)
 
 
-def _kv8(rt, cache, dev, what: str = "cache"):
-    """Checks a cache's tensors on device `dev`: (its four addresses, B, Hkv,
-    capacity, D, block, code)."""
-    k, v, ks, vs = cache
-    shape, code = k.shape, rt.codes.get(k.dtype)
-    if code is None or len(shape) != 4 or ks.dim() != 3 or ks.shape[2] == 0 or shape[2] % ks.shape[2]:
-        raise ValueError(f"{what}: codes are int8 or float8_e4m3fn [B, Hkv, capacity, D], scales [B, Hkv, capacity / block]")
-    B, Hkv, capacity, D = shape
-    blocks = (B, Hkv, ks.shape[2])
-    at = (_arg(what + ".k", k, shape, k.dtype, dev), _arg(what + ".v", v, shape, k.dtype, dev),
-          _arg(what + ".k_scale", ks, blocks, rt.float32, dev), _arg(what + ".v_scale", vs, blocks, rt.float32, dev))
-    return at, B, Hkv, capacity, D, capacity // blocks[2], code
-
-
 def kv8_append(cache: KV8Cache, k, v, start, num_new=None, layout: str = "HND", cu_seqlens=None,
                max_seqlen: Optional[int] = None, stream=None) -> KV8Cache:
     """Quantises new tokens into the cache, in place.
@@ -711,27 +642,7 @@ def kv8_append(cache: KV8Cache, k, v, start, num_new=None, layout: str = "HND", 
     first num_new[b] tokens only (dense layouts).  Positions and counts are
     clamped on the device; tokens behind the capacity are dropped.  A block's
     scale grows with its largest value and its older codes follow."""
-    rt = _runtime()
-    dt, dev = k.dtype, k.get_device()
-    at, B, Hkv, capacity, D, block, code = _kv8(rt, cache, dev)
-    T = 0
-    if layout == "TND":
-        if cu_seqlens is None or max_seqlen is None or num_new is not None or k.dim() != 3:
-            raise ValueError("TND rows are [tokens, heads, D], with cu_seqlens and max_seqlen and without num_new")
-        T, S = k.shape[0], int(max_seqlen)
-        shape = (T, Hkv, D)
-    else:
-        if layout not in LAYOUTS or cu_seqlens is not None or max_seqlen is not None or k.dim() != 4:
-            raise ValueError(f"layout {layout!r}: rows are 4-D, without cu_seqlens and max_seqlen")
-        S = k.shape[2 if layout == "HND" else 1]
-        shape = (B, Hkv, S, D) if layout == "HND" else (B, S, Hkv, D)
-    pk, pv = _arg("k", k, shape, dt, dev), _arg("v", v, shape, dt, dev)
-    ps = _arg("start", start, (B,), rt.int32, dev)
-    pn, pc = _opt("num_new", num_new, (B,), rt.int32, dev), _opt("cu_seqlens", cu_seqlens, (B + 1,), rt.int32, dev)
-    half = _half(rt, dt, "k")
-    if S and (T or layout != "TND"):
-        _call(rt, "kv8_append", dev, stream, pk, pv, *at, ps, pn, pc, B, Hkv, S, T, capacity, D, block, half, code,
-              LAYOUTS[layout])
+    _torch_calls().kv8_append(cache, k, v, start, num_new, _layout(layout), cu_seqlens, max_seqlen, _handle(stream))
     return cache
 
 
@@ -740,25 +651,7 @@ def kv8_fetch(cache: KV8Cache, n: int, dtype=None, start=None, kv_len=None, layo
     """A window of n tokens of every sequence in 16 bits: (k, v) [B,Hkv,n,D] (HND)
     or [B,n,Hkv,D] (NHD), token i from position start[b] + i (start: int32 device
     tensor [B], default 0); zero at positions outside [0, kv_len[b])."""
-    rt = _runtime()
-    dev = cache.k.get_device()
-    at, B, Hkv, capacity, D, block, code = _kv8(rt, cache, dev)
-    if layout not in ("HND", "NHD") or n < 0:
-        raise ValueError(f"kv8_fetch takes HND or NHD, not {layout!r}, and n >= 0, not {n}")
-    shape = (B, Hkv, n, D) if layout == "HND" else (B, n, Hkv, D)
-    if dtype is None:
-        dtype = k_out.dtype if k_out is not None else rt.torch.bfloat16
-    half = _half(rt, dtype, "dtype")
-    ps, pl = _opt("start", start, (B,), rt.int32, dev), _opt("kv_len", kv_len, (B,), rt.int32, dev)
-    if k_out is None:
-        k_out = rt.empty(shape, dtype=dtype, device=cache.k.device)
-    if v_out is None:
-        v_out = rt.empty_like(k_out)
-    pk, pv = _arg("k_out", k_out, shape, dtype, dev), _arg("v_out", v_out, shape, dtype, dev)
-    if n:
-        _call(rt, "kv8_fetch", dev, stream, *at, pk, pv, ps, pl, B, Hkv, int(n), capacity, D, block, half, code,
-              LAYOUTS[layout])
-    return k_out, v_out
+    return _torch_calls().kv8_fetch(cache, n, dtype, start, kv_len, _layout(layout), k_out, v_out, _handle(stream))
 
 
 def attn_splitkv_kv8_plan(B: int, Hq: int, Hkv: int, Lq: int, capacity: int, D: int = 128, num_sms: int = 148,
@@ -775,14 +668,6 @@ def attn_splitkv_kv8_workspace(B: int, Hq: int, Lq: int, capacity: int, D: int, 
     return int(lib().attn_splitkv_kv8_workspace(B, Hq, Lq, capacity, D, num_splits, int(bool(weights))))
 
 
-@functools.lru_cache(maxsize=256)
-def _kv8_plan(B, Hq, Hkv, Lq, capacity, D, requested, weights, device):
-    """(splits, workspace bytes): a function of the sizes and the device's SM count."""
-    sms = _runtime().torch.cuda.get_device_properties(device).multi_processor_count
-    splits = attn_splitkv_kv8_plan(B, Hq, Hkv, Lq, capacity, D, sms, requested)
-    return splits, attn_splitkv_kv8_workspace(B, Hq, Lq, capacity, D, splits, weights)
-
-
 def attn_splitkv_decode_kv8(q, cache: KV8Cache, scale: Optional[float] = None, kv_len=None, causal: bool = False,
                             weights=None, num_splits: int = 0, out=None, lse=None, return_lse: bool = True,
                             workspace=None, stream=None):
@@ -792,31 +677,8 @@ def attn_splitkv_decode_kv8(q, cache: KV8Cache, scale: Optional[float] = None, k
     weights: optional float32 [B,Hkv,capacity]; each visible key's attention
     weight, summed over the query rows of its kv head, is added to it (for
     kv8_evict).  Returns (out, lse)."""
-    rt = _runtime()
-    shape, dt, dev = q.shape, q.dtype, q.get_device()
-    at, B, Hkv, capacity, D, block, code = _kv8(rt, cache, dev)
-    if len(shape) != 4:
-        raise ValueError("decode q is [B, Hq, Lq, D]")
-    Hq, Lq = shape[1], shape[2]
-    pq, half = _arg("q", q, (B, Hq, Lq, D), dt, dev), _half(rt, dt, "q")
-    pn = _opt("kv_len", kv_len, (B,), rt.int32, dev)
-    pw = _opt("weights", weights, (B, Hkv, capacity), rt.float32, dev)
-    splits, need = _kv8_plan(B, Hq, Hkv, Lq, capacity, D, int(num_splits), pw is not None, dev)
-    if out is None:
-        out = rt.empty_like(q)
-    if not return_lse:
-        lse = None
-    elif lse is None:
-        lse = rt.empty((B, Hq, Lq), dtype=rt.float32, device=q.device)
-    if workspace is None and need:
-        workspace = rt.empty(need, dtype=rt.torch.uint8, device=q.device)
-    ws, wbytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    if workspace is not None and workspace.get_device() != dev:
-        raise ValueError(f"workspace is on {workspace.device}, q on {q.device}")
-    _call(rt, "attn_splitkv_decode_kv8", dev, stream, pq, *at, _arg("out", out, shape, dt, dev),
-          _opt("lse", lse, (B, Hq, Lq), rt.float32, dev), pw, B, Hq, Hkv, Lq, capacity, D, block,
-          float(D ** -0.5 if scale is None else scale), half, code, pn, 1 if causal else 0, splits, ws, wbytes)
-    return out, lse
+    return _torch_calls().decode_kv8(q, cache, scale, kv_len, causal, weights, num_splits, out, lse, return_lse, workspace,
+                                     _handle(stream))
 
 
 def kv8_evict(cache: KV8Cache, to: KV8Cache, weights, to_weights, kv_len, budget: int, sink: int = 0, recent: int = 0,
@@ -827,25 +689,8 @@ def kv8_evict(cache: KV8Cache, to: KV8Cache, weights, to_weights, kv_len, budget
     cache that shares no memory with this one) with their weights into
     `to_weights`.  kv_len: int32 device tensor [B] or None (the capacity).
     Returns (kept int32 [B,Hkv,budget], -1 behind the last; new_len int32 [B])."""
-    rt = _runtime()
-    dev = cache.k.get_device()
-    at, B, Hkv, capacity, D, block, code = _kv8(rt, cache, dev)
-    to_at, B2, H2, to_capacity, D2, block2, code2 = _kv8(rt, to, dev, "to")
-    if (B2, H2, D2, block2, code2) != (B, Hkv, D, block, code):
-        raise ValueError("the two caches differ in more than their capacity")
-    if not (1 <= budget <= to_capacity and sink >= 0 and recent >= 0 and sink + recent <= budget):
-        raise ValueError(f"budget {budget} must fit the capacity {to_capacity} and hold sink {sink} + recent {recent}")
-    pw = _arg("weights", weights, (B, Hkv, capacity), rt.float32, dev)
-    pt = _arg("to_weights", to_weights, (B, Hkv, to_capacity), rt.float32, dev)
-    pl = _opt("kv_len", kv_len, (B,), rt.int32, dev)
-    if kept is None:
-        kept = rt.empty((B, Hkv, budget), dtype=rt.int32, device=weights.device)
-    if new_len is None:
-        new_len = rt.empty((B,), dtype=rt.int32, device=weights.device)
-    _call(rt, "kv8_evict", dev, stream, *at, pw, pl, *to_at, pt, _arg("kept", kept, (B, Hkv, budget), rt.int32, dev),
-          _arg("new_len", new_len, (B,), rt.int32, dev), B, Hkv, capacity, to_capacity, D, block, code, int(budget),
-          int(sink), int(recent))
-    return kept, new_len
+    return _torch_calls().kv8_evict(cache, to, weights, to_weights, kv_len, budget, sink, recent, kept, new_len,
+                                    _handle(stream))
 
 
 __all__ = ["attn_fwd_lse", "attn_fwd_lse_chunks", "attn_fwd_lse_chunks_workspace", "attn_fwd_lse_int8", "attn_splitkv_decode", "attn_splitkv_decode_static", "merge_state",

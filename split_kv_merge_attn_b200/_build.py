@@ -1,7 +1,9 @@
-"""Builds the in-tree shared library ``libsplitkv.so`` for sm_100a with nvcc.
+"""Builds the in-tree shared library ``libsplitkv.so`` for sm_100a with nvcc, and
+``_skv_torch.so``, the extension module that marshals PyTorch tensors for the
+short calls, with the host compiler.
 
-Usage: ``python -m split_kv_merge_attn_b200._build`` (or ``build()``).  The
-library is written next to this file so it travels with the source tree.
+Usage: ``python -m split_kv_merge_attn_b200._build`` (or ``build()``).  Both are
+written next to this file so they travel with the source tree.
 """
 from __future__ import annotations
 
@@ -15,6 +17,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libsplitkv.so")
+TORCH_LIB = os.path.join(HERE, "_skv_torch.so")
 
 SOURCES = ["skv_kernels.cu", "skv_abi.cpp", "skv_noalloc.cu", "skv_cache.cu"]
 HEADERS = ["skv_device.cuh", "skv_internal.h", "merge_state.cuh", "decode.cuh", "prefill.cuh",
@@ -39,26 +42,45 @@ def command(out: str = LIB, extra=None):
     return cmd
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB):
+def torch_command(out: str = TORCH_LIB):
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    root = os.path.dirname(torch.__file__)
+    include = cpp_extension.include_paths() + [os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"),
+                                               sysconfig.get_paths()["include"]]
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++20", "-fPIC", "-shared", "-Wall", "-I", INCLUDE]
+    for p in include:
+        cmd += ["-isystem", p]
+    cmd += [os.path.join(CSRC, "skv_torch.cpp"), "-o", out, "-L", os.path.join(root, "lib")]
+    return cmd + ["-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-ltorch", "-lc10_cuda", "-lc10"]
+
+
+def _stale(lib: str, deps) -> bool:
+    if not os.path.exists(lib):
         return True
-    t = os.path.getmtime(LIB)
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(INCLUDE, "splitkv.h"), __file__]
+    t = os.path.getmtime(lib)
+    deps = [os.path.join(CSRC, f) for f in deps] + [os.path.join(INCLUDE, "splitkv.h"), __file__]
     return any(os.path.getmtime(d) > t for d in deps if os.path.exists(d))
 
 
-def build(force: bool = False, verbose: bool = False, extra=None) -> str:
-    if not force and not _stale():
-        return LIB
-    cmd = command(extra=extra)
+def _run(cmd, name: str, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError("nvcc failed building libsplitkv.so")
+        raise RuntimeError(f"building {name} failed")
     if verbose and (r.stdout or r.stderr):
         print(r.stdout + r.stderr)
+
+
+def build(force: bool = False, verbose: bool = False, extra=None) -> str:
+    if force or _stale(LIB, SOURCES + HEADERS):
+        _run(command(extra=extra), "libsplitkv.so", verbose)
+    if force or _stale(TORCH_LIB, ["skv_torch.cpp"]):
+        _run(torch_command(), "_skv_torch.so", verbose)
     return LIB
 
 
