@@ -458,29 +458,32 @@ skv_status kv8_fetch(const void* k_codes, const void* v_codes, const float* k_sc
 
 /* attn_splitkv_decode_kv8: attn_splitkv_decode over the 8-bit cache.
  *
- * O, LSE, kv_len, causal (as attn_splitkv_decode_causal), num_splits and the
- * split rule are those of attn_splitkv_decode with K = codes * scale and
- * V = codes * scale; the products take the codes exactly.  A non-finite scale
- * makes the rows that see its block NaN.
+ * O, LSE, kv_len and causal (as attn_splitkv_decode_causal) are those of
+ * attn_splitkv_decode with K = codes * scale and V = codes * scale; the products
+ * take the codes exactly.  A non-finite scale makes the rows that see its block
+ * NaN.  num_ctas: the keys of all sequences and heads are divided evenly among
+ * this many CTAs, 1..1024 (0 = automatic, attn_splitkv_kv8_plan with the device's
+ * SM count); the division follows kv_len on the device.
  * weights: device fp32 [B, Hkv, capacity] (16-byte aligned) or NULL.  If given,
  * each visible key's attention weight is added to it: weights[b, h, j] += sum
  * over the G * Lq query rows of kv head h of exp(s_j) / sum exp(s), one addition
  * per entry and call; entries >= kv_len[b] stay as they are.
  * workspace: device, 256-byte aligned, >= attn_splitkv_kv8_workspace(...) bytes
- * for the split count used (with weights: the rows' logits, 4 * B * Hq * Lq *
- * capacity bytes). */
+ * for the CTA count used (with weights it holds the rows' logits, 4 * B * Hq * Lq *
+ * capacity bytes).  Nothing in it needs to start at zero. */
 skv_status attn_splitkv_decode_kv8(const void* q, const void* k_codes, const void* v_codes, const float* k_scale,
                                    const float* v_scale, void* out, float* lse, float* weights, int B, int Hq, int Hkv,
                                    int Lq, int capacity, int D, int block, float scale, skv_dtype dtype,
-                                   skv_code codes, const int32_t* kv_len, int causal, int num_splits, void* workspace,
+                                   skv_code codes, const int32_t* kv_len, int causal, int num_ctas, void* workspace,
                                    size_t workspace_bytes, skv_stream_t stream);
 
-/* Split count of the 8-bit decode (host): requested_splits if > 0, else as many
- * as give about two CTAs per SM over the B * Hkv * ceil(G * Lq / 16) units of
- * one split, with at least 128 keys each (the kernel's CTAs come two to an SM). */
+/* CTA count of the 8-bit decode (host): requested_ctas if > 0, else two per SM,
+ * but no more than there is work for at the full capacity: for each batch entry,
+ * kv head and 16 of its query rows, one more than its tiles of 256 keys (64 at
+ * D = 256). */
 skv_status attn_splitkv_kv8_plan(int B, int Hq, int Hkv, int Lq, int capacity, int D, int num_sms,
-                                 int requested_splits, int* num_splits);
-size_t attn_splitkv_kv8_workspace(int B, int Hq, int Lq, int capacity, int D, int num_splits, int weights);
+                                 int requested_ctas, int* num_ctas);
+size_t attn_splitkv_kv8_workspace(int B, int Hq, int Hkv, int Lq, int capacity, int D, int num_ctas, int weights);
 
 /* kv8_evict: cuts each sequence to `budget` tokens by accumulated weight.
  *

@@ -75,7 +75,7 @@ SIGNATURES = {
     "kv8_append": (_c_int, [_vp] * 9 + [_c_int] * 10 + [_vp]),
     "kv8_fetch": (_c_int, [_vp] * 8 + [_c_int] * 9 + [_vp]),
     "attn_splitkv_kv8_plan": (_c_int, [_c_int] * 8 + [_vp]),
-    "attn_splitkv_kv8_workspace": (_c_size, [_c_int] * 7),
+    "attn_splitkv_kv8_workspace": (_c_size, [_c_int] * 8),
     "attn_splitkv_decode_kv8": (_c_int, [_vp] * 8 + [_c_int] * 7 + [_c_float, _c_int, _c_int, _vp, _c_int, _c_int, _vp,
                                                                     _c_size, _vp]),
     "kv8_evict": (_c_int, [_vp] * 13 + [_c_int] * 10 + [_vp]),
@@ -655,29 +655,30 @@ def kv8_fetch(cache: KV8Cache, n: int, dtype=None, start=None, kv_len=None, layo
 
 
 def attn_splitkv_kv8_plan(B: int, Hq: int, Hkv: int, Lq: int, capacity: int, D: int = 128, num_sms: int = 148,
-                          requested_splits: int = 0) -> int:
-    """Split count of attn_splitkv_decode_kv8."""
+                          requested_ctas: int = 0) -> int:
+    """CTA count of attn_splitkv_decode_kv8."""
     ns = ctypes.c_int(0)
-    _check(lib().attn_splitkv_kv8_plan(B, Hq, Hkv, Lq, capacity, D, num_sms, requested_splits, ctypes.byref(ns)),
+    _check(lib().attn_splitkv_kv8_plan(B, Hq, Hkv, Lq, capacity, D, num_sms, requested_ctas, ctypes.byref(ns)),
            "attn_splitkv_kv8_plan")
     return ns.value
 
 
-def attn_splitkv_kv8_workspace(B: int, Hq: int, Lq: int, capacity: int, D: int, num_splits: int,
+def attn_splitkv_kv8_workspace(B: int, Hq: int, Hkv: int, Lq: int, capacity: int, D: int, num_ctas: int,
                                weights: bool = False) -> int:
-    return int(lib().attn_splitkv_kv8_workspace(B, Hq, Lq, capacity, D, num_splits, int(bool(weights))))
+    return int(lib().attn_splitkv_kv8_workspace(B, Hq, Hkv, Lq, capacity, D, num_ctas, int(bool(weights))))
 
 
 def attn_splitkv_decode_kv8(q, cache: KV8Cache, scale: Optional[float] = None, kv_len=None, causal: bool = False,
-                            weights=None, num_splits: int = 0, out=None, lse=None, return_lse: bool = True,
+                            weights=None, num_ctas: int = 0, out=None, lse=None, return_lse: bool = True,
                             workspace=None, stream=None):
     """attn_splitkv_decode over the 8-bit cache: q [B,Hq,Lq,D] (bf16 or fp16),
     kv_len optional int32 device tensor [B] (default: the capacity).  causal:
     query row i of Lq sees the first kv_len - Lq + 1 + i keys.
     weights: optional float32 [B,Hkv,capacity]; each visible key's attention
     weight, summed over the query rows of its kv head, is added to it (for
-    kv8_evict).  Returns (out, lse)."""
-    return _torch_calls().decode_kv8(q, cache, scale, kv_len, causal, weights, num_splits, out, lse, return_lse, workspace,
+    kv8_evict).  num_ctas: the CTAs the keys are divided among (0: two per SM).
+    Returns (out, lse)."""
+    return _torch_calls().decode_kv8(q, cache, scale, kv_len, causal, weights, num_ctas, out, lse, return_lse, workspace,
                                      _handle(stream))
 
 

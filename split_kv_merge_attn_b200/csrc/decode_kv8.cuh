@@ -1,5 +1,12 @@
-// Split-KV decode over the 8-bit cache: per (batch entry, kv head, group of 16
-// query rows, split) one CTA streams its split's codes from HBM exactly once.
+// Split-KV decode over the 8-bit cache.  The keys of every unit (batch entry, kv
+// head, group of 16 query rows) form tiles; all units' tiles in a row are divided
+// evenly among the CTAs, two to an SM, whatever the sequences' lengths.  A CTA's
+// share is one or more segments of units; it streams each segment's codes from HBM
+// exactly once and writes the unit's result where the segment is all of it, else a
+// partial (O, LSE) that kv8_merge_kernel joins.  (Equal splits of each sequence
+// left SMs idle where lengths differ or units do not divide the SMs: B = 16, 16
+// heads, D = 64, lengths 4096 to 16384: 89 us with one split, 74 with the best,
+// 65 so.)
 //
 // With code blocks of scales ks, vs (one per block of tokens and head):
 //   x_j = scale * log2(e) * ks_j * (q . ck_j),  p_j = 2^(x_j - m),  m = max x_j
@@ -47,7 +54,8 @@ template <int D>
 struct Kv8DecodeCfg {
   static constexpr int kKeys = D == 64 ? 64 : (D == 128 ? 32 : 16);  // keys of a load (4 KB of K, 4 KB of V)
   static constexpr int kLoads = D == 128 ? 2 : 1;              // loads of one softmax tile
-  static constexpr int kTileKeys = kKeys * kLoads;
+  static constexpr int kTileKeys = kKeys * kLoads;             // of a warp
+  static constexpr int kCtaKeys = kKv8Warps * kTileKeys;       // a tile of the division among CTAs
   static constexpr int kTileBytes = kKeys * D;                 // one load of K or V
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kBoxes = D == 256 ? 2 : 1;              // 128-byte wide boxes
@@ -67,17 +75,39 @@ struct Kv8DecodeArgs {
   const void* q;
   void* out;
   float* lse;
-  float* part_o;
-  float* part_lse;
+  uint32_t* table;         // [B + 1] places (of one head and row group) of the sequences before each, for the
+                           // merge, where kv_len is given and units can be divided; else null
+  float* part_o;           // [slots, 16, D]
+  float* part_lse;         // [slots, 16]
   float* logits;           // [B, Hkv, G * Lq, capacity] log2-domain logits, or null
   const float* k_scale;
   const float* v_scale;
   const int* kv_len;
   int B, Hq, Hkv, Lq, capacity, block_shift;
-  int num_splits;
   int row_groups;
   int causal;
   float scale_log2;
+};
+
+// How `total` places are divided among `ctas` CTAs (no more than places): the
+// first `rest` of them take quota + 1, the others quota.  A unit of T > 0 tiles has
+// T + 1 places: one before its first tile, for the time a CTA takes to change
+// units (about a tile's), which holds no keys.  Segment (c, unit u) has partial
+// slot c + u: along the places either grows by one.
+struct Kv8Division {
+  uint32_t ctas, quota, rest;
+  __device__ __forceinline__ Kv8Division(uint32_t total, uint32_t most) {
+    ctas = max(1u, min(most, total));
+    quota = total / ctas;
+    rest = total - quota * ctas;
+  }
+  // first place of CTA c's share
+  __device__ __forceinline__ uint32_t begin(uint32_t c) const { return min(c, ctas) * quota + min(c, rest); }
+  // the CTA that has place t
+  __device__ __forceinline__ uint32_t owner(uint32_t t) const {
+    const uint32_t big = rest * (quota + 1);
+    return t < big ? t / (quota + 1) : rest + (t - big) / quota;
+  }
 };
 
 // A word of codes {a, b, c, d} -> fp16 pairs (a, b) and (c, d).  int8: 0x6400 | u
@@ -180,12 +210,12 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
   uint64_t* full_v = full_k + Cfg::kStages;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::kRingBytes + Cfg::kQBytes +
                                                              kKv8Warps * 2 * Cfg::kStages * 8);
-  const int split = blockIdx.x;
   const int G = a.Hq / a.Hkv;
   const int rows_total = G * a.Lq;
-  const int rg = blockIdx.y % a.row_groups;
-  const int hkv = (blockIdx.y / a.row_groups) % a.Hkv;
-  const int b = blockIdx.y / (a.row_groups * a.Hkv);
+  const int heads = a.Hkv * a.row_groups;  // units of a sequence
+  __shared__ uint32_t scan[kKv8Warps];
+  __shared__ uint32_t s_base;
+  __shared__ int s_b;
 
   if (lane == 0) {
     for (int s = 0; s < 2 * Cfg::kStages; ++s) mbar_init(&full_k[s], 1);
@@ -197,21 +227,104 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  int n = a.capacity;
-  if (a.kv_len != nullptr) n = min(max(a.kv_len[b], 0), a.capacity);
-  int s0 = 0, s1 = 0;
-  if (n > 0) {  // the split rule of the host planner
-    const int per = (n + a.num_splits - 1) / a.num_splits;
-    const int C = ((per + 63) / 64) * 64;
-    const int64_t lo = static_cast<int64_t>(split) * C;
-    s0 = static_cast<int>(min(lo, static_cast<int64_t>(n)));
-    s1 = static_cast<int>(min(lo + C, static_cast<int64_t>(n)));
+  constexpr int kTileKeys = Cfg::kTileKeys;
+  constexpr int kStride = Cfg::kCtaKeys;
+  auto length = [&](int b) { return a.kv_len != nullptr ? min(max(__ldg(a.kv_len + b), 0), a.capacity) : a.capacity; };
+  auto tiles = [](int n) { return (n + kStride - 1) / kStride; };
+  auto places = [&](int n) { return n > 0 ? static_cast<uint32_t>(tiles(n)) + 1 : 0u; };
+  // ---- this CTA's places [w, w1), and the sequence the first lies in: b, whose
+  // places begin at `base`
+  uint32_t w, w1, base;
+  int b;
+  if (a.kv_len == nullptr) {
+    const uint32_t each = places(a.capacity) * heads;
+    const Kv8Division division(each * a.B, gridDim.x);
+    w = division.begin(blockIdx.x);
+    w1 = division.begin(blockIdx.x + 1);
+    b = static_cast<int>(w / each);
+    base = b * each;
+  } else {
+    // thread i sums the places of sequences i * per ...
+    const int per = (a.B + kKv8Threads - 1) / kKv8Threads;
+    const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+    uint32_t mine = 0;
+    for (int i = b0; i < b1; ++i) mine += places(length(i));
+    uint32_t before = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t v = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += v;
+    }
+    if (lane == 31) scan[warp] = before;
+    __syncthreads();
+    before -= mine;
+    uint32_t total = 0;
+#pragma unroll
+    for (int i = 0; i < kKv8Warps; ++i) {
+      if (i < warp) before += scan[i];
+      total += scan[i];
+    }
+    const Kv8Division division(total * heads, gridDim.x);
+    w = division.begin(blockIdx.x);
+    w1 = division.begin(blockIdx.x + 1);
+    if (w >= before * heads && w < (before + mine) * heads) {
+      uint32_t at = before;
+      int i = b0;
+      for (; i < b1; ++i) {
+        const uint32_t t = places(length(i));
+        if (w < (at + t) * heads) break;
+        at += t;
+      }
+      s_b = i;
+      s_base = at * heads;
+    }
+    if (a.table != nullptr && blockIdx.x == 0) {
+      for (int i = b0; i < b1; ++i) {
+        a.table[i] = before;
+        before += places(length(i));
+      }
+      if (tid == 0) a.table[a.B] = total;
+    }
+    __syncthreads();
+    b = s_b;       // (not set, and not used, where the share is empty)
+    base = s_base;
   }
+  // units without keys: O = 0, LSE = -inf
+  if (a.kv_len != nullptr) {
+    for (int64_t u = blockIdx.x; u < static_cast<int64_t>(a.B) * heads; u += gridDim.x) {
+      const int ub = static_cast<int>(u / heads), uh = static_cast<int>(u - static_cast<int64_t>(ub) * heads);
+      if (length(ub) > 0) continue;
+      const int r0 = uh % a.row_groups * kKv8Rows, rn = min(kKv8Rows, rows_total - r0);
+      const int64_t row = (static_cast<int64_t>(ub) * a.Hq + static_cast<int64_t>(uh / a.row_groups) * G) * a.Lq + r0;
+      for (int i = tid; i < rn * (D / 8); i += kKv8Threads)
+        reinterpret_cast<uint4*>(static_cast<T*>(a.out) + row * D)[i] = make_uint4(0, 0, 0, 0);
+      if (a.lse != nullptr && tid < rn) a.lse[row + tid] = -INFINITY;
+    }
+  }
+
+  const int g = lane >> 2, tq = lane & 3;
+  int st_k = 0, st_v = 0;            // stages of the next K and V load to be read
+  uint32_t phase_k = 0, phase_v = 0;
+  int seen = 0;                      // loads of the segments before
+  while (w < w1) {
+  const int n = length(b);
+  const uint32_t unit_places = places(n);
+  if (w >= base + unit_places * heads) {  // the next sequence
+    base += unit_places * heads;
+    ++b;
+    continue;
+  }
+  const int uh = static_cast<int>((w - base) / unit_places);
+  const uint32_t p0 = w - base - uh * unit_places, p1 = min(unit_places, p0 + (w1 - w));
+  w += p1 - p0;
+  const int t_first = max(static_cast<int>(p0), 1) - 1, t_end = static_cast<int>(p1) - 1;
+  if (t_end <= t_first) continue;         // only the place without keys
+  const bool whole_unit = t_end - t_first == tiles(n);
+  const int hkv = uh / a.row_groups, rg = uh - hkv * a.row_groups;
+  const int s0 = t_first * kStride, s1 = min(n, t_end * kStride);
   const int64_t bh = static_cast<int64_t>(b) * a.Hkv + hkv;
   // this warp's tiles: keys first + t * kStride; loads u = kLoads * t + i of their
   // kKeys keys, the last ones of which may lie behind the end
-  constexpr int kTileKeys = Cfg::kTileKeys;
-  constexpr int kStride = kKv8Warps * kTileKeys;
   const int first = s0 + warp * kTileKeys;
   const int ntiles = first < s1 ? (s1 - first + kStride - 1) / kStride : 0;
   const int nloads = ntiles * Cfg::kLoads;
@@ -227,14 +340,14 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
     for (int bx = 0; bx < Cfg::kBoxes; ++bx) tma_load_2d(dst + bx * kKeys * 128, map, &full[st], bx * 128, row);
   };
   if (lane == 0) {
+    int st = st_k;  // = st_v between segments
     for (int u = 0; u < min(nloads, Cfg::kStages); ++u) {
-      load(u, u, &tmK, 0, full_k);
-      load(u, u, &tmV, 1, full_v);
+      load(u, st, &tmK, 0, full_k);
+      load(u, st, &tmV, 1, full_v);
+      if (++st == Cfg::kStages) st = 0;
     }
   }
   __syncwarp();
-
-  const int g = lane >> 2, tq = lane & 3;
 
   // ---- Q fragments: rows g and g + 8, this thread's share of every key row
   // (32 contiguous values per box at 32 tq; 16 at 16 tq for D = 64)
@@ -389,8 +502,6 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
   auto wait = [&](uint64_t* full, uint32_t phase) {
     return __all_sync(0xffffffffu, mbar_wait(full, phase, abort_flag, kErrKv8FullWait)) != 0;
   };
-  int st_k = 0, st_v = 0;
-  uint32_t phase_k = 0, phase_v = 0;
   int uk = 0, uv = 0;  // loads of K and of V read so far
   bool ok = true;
   for (int key0 = first; key0 < s1; key0 += kStride) {
@@ -562,11 +673,13 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
   }
   if (uv < nloads && lane == 0) {
     // a wait gave up: let the loads already issued land before the shared memory goes away
-    for (int u = uk; u < min(nloads, uk + Cfg::kStages); ++u)
+    for (int u = seen + uk; u < seen + min(nloads, uk + Cfg::kStages); ++u)
       mbar_drain(&full_k[u % Cfg::kStages], (u / Cfg::kStages) & 1, 20000000ull);
-    for (int u = uv; u < min(nloads, uv + Cfg::kStages); ++u)
+    for (int u = seen + uv; u < seen + min(nloads, uv + Cfg::kStages); ++u)
       mbar_drain(&full_v[u % Cfg::kStages], (u / Cfg::kStages) & 1, 20000000ull);
   }
+
+  seen += nloads;
 
   // ---- combine the four warps' states
   __syncthreads();
@@ -600,9 +713,9 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
   // Per row: M = max_w m_w, L = sum_w 2^(m_w - M) l_w; O = sum_w 2^(mv_w - M) O_w / L
   // (2^(mv_w - M) <= the largest vs: finite), LSE = M + log2 L.
   const int rows_here = min(kKv8Rows, rows_total - rg * kKv8Rows);
-  const int64_t rows_all = static_cast<int64_t>(a.B) * a.Hq * a.Lq;
   const int64_t orow0 = (static_cast<int64_t>(b) * a.Hq + static_cast<int64_t>(hkv) * G) * a.Lq +
                         static_cast<int64_t>(rg) * kKv8Rows;
+  const int64_t slot = (blockIdx.x + static_cast<int64_t>(b) * heads + uh) * kKv8Rows;
 #pragma unroll
   for (int hr = 0; hr < 2; ++hr) {
     const int r = g + 8 * hr;
@@ -623,12 +736,12 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
     for (int w = 0; w < kKv8Warps; ++w) wt[w] *= inv;
     if (warp == 0 && tq == 0) {
       const float lse = L == 0.f ? -INFINITY : M + __log2f(L);
-      if (a.num_splits == 1) {
+      if (whole_unit) {
         if (a.lse != nullptr) a.lse[orow0 + r] = lse;
       } else {
         // a NaN partial is handed on as +inf: the merge's maximum would drop a
         // NaN and take the row for empty, while 2^(inf - inf) keeps it
-        a.part_lse[static_cast<int64_t>(split) * rows_all + orow0 + r] = isnan(lse) ? INFINITY : lse;
+        a.part_lse[slot + r] = isnan(lse) ? INFINITY : lse;
       }
     }
 #pragma unroll
@@ -644,12 +757,125 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
         acc.w = fmaf(wt[w], v.w, acc.w);
       }
       const int d = 16 * c + 4 * tq;
-      if (a.num_splits == 1)
+      if (whole_unit)
         *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (orow0 + r) * D + d) =
             make_uint2(pack2<T>(acc.x, acc.y), pack2<T>(acc.z, acc.w));
       else
-        *reinterpret_cast<float4*>(a.part_o + (static_cast<int64_t>(split) * rows_all + orow0 + r) * D + d) = acc;
+        *reinterpret_cast<float4*>(a.part_o + (slot + r) * D + d) = acc;
     }
+  }
+  // the next segment's loads may overwrite what the combine has just read and written
+  fence_proxy_async_smem();
+  __syncthreads();
+  }
+}
+
+// Joins the partials of each row whose unit is divided: parts c0 + u .. c1 + u of
+// unit u, one CTA a row, its threads over columns and parts.  M = max_p L_p,
+// w_p = 2^(L_p - M), O = sum w_p O_p / sum w_p, LSE = M + log2 sum w_p.
+constexpr int kKv8MaxCtas = 1024;
+
+template <int D, typename T>
+__global__ void __launch_bounds__(256) kv8_merge_kernel(const Kv8DecodeArgs a, int ctas) {
+  constexpr int kStride = Kv8DecodeCfg<D>::kCtaKeys;
+  constexpr int kCols = D / 4;          // of four values
+  constexpr int kLanes = 256 / kCols;   // threads of a column, each with every kLanes-th part
+  constexpr int kFlight = 4;
+  __shared__ float weight[kKv8MaxCtas];
+  __shared__ float4 sums[256];
+  __shared__ float red[16];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x, G = a.Hq / a.Hkv, heads = a.Hkv * a.row_groups;
+  const int row = blockIdx.x;           // (b, h, i)
+  const int h = row / a.Lq % a.Hq, b = row / a.Lq / a.Hq;
+  const int r = h % G * a.Lq + row % a.Lq;  // of the kv head's rows
+  const int uh = h / G * a.row_groups + r / kKv8Rows;
+  uint32_t before, unit_places, total;
+  if (a.kv_len == nullptr) {
+    unit_places = static_cast<uint32_t>((a.capacity + kStride - 1) / kStride) + 1;
+    before = b * unit_places;
+    total = a.B * unit_places;
+  } else {
+    before = __ldg(a.table + b);
+    unit_places = __ldg(a.table + b + 1) - before;
+    total = __ldg(a.table + a.B);
+  }
+  if (unit_places == 0) return;         // no keys: written by the split kernel
+  const Kv8Division division(total * heads, ctas);
+  const uint32_t t0 = before * heads + uh * unit_places;
+  const uint32_t c0 = division.owner(t0 + 1);
+  const int parts = static_cast<int>(division.owner(t0 + unit_places - 1) - c0) + 1;
+  if (parts == 1) return;               // whole: written by the split kernel
+  const int64_t slot = (c0 + static_cast<int64_t>(b) * heads + uh) * kKv8Rows + r % kKv8Rows;
+  const float* L = a.part_lse + slot;
+  const int col = tid % kCols, lane = tid / kCols;
+  const float4* O = reinterpret_cast<const float4*>(a.part_o + slot * D) + col;
+  constexpr int64_t kStep = kKv8Rows * D / 4;  // float4s from one part to the next
+  float4 x[kFlight];
+#pragma unroll
+  for (int i = 0; i < kFlight; ++i) {
+    const int p = lane + i * kLanes;
+    if (p < parts) x[i] = __ldg(O + p * kStep);
+  }
+  float top = -INFINITY;
+  for (int p = tid; p < parts; p += 256) {
+    const float v = __ldg(L + static_cast<int64_t>(p) * kKv8Rows);
+    weight[p] = v;
+    top = fmaxf(top, v);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if ((tid & 31) == 0) red[tid >> 5] = top;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = fmaxf(top, red[i]);
+  float sum = 0.f;
+  for (int p = tid; p < parts; p += 256) {
+    const float v = weight[p] == -INFINITY ? 0.f : ex2_approx(weight[p] - top);
+    weight[p] = v;
+    sum += v;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if ((tid & 31) == 0) red[8 + (tid >> 5)] = sum;
+  __syncthreads();
+  sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sum += red[8 + i];
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int p0 = lane; p0 < parts; p0 += kFlight * kLanes) {
+#pragma unroll
+    for (int i = 0; i < kFlight; ++i) {
+      const int p = p0 + i * kLanes;
+      if (p >= parts) break;
+      const float v = weight[p];
+      acc.x = fmaf(v, x[i].x, acc.x);
+      acc.y = fmaf(v, x[i].y, acc.y);
+      acc.z = fmaf(v, x[i].z, acc.z);
+      acc.w = fmaf(v, x[i].w, acc.w);
+    }
+#pragma unroll
+    for (int i = 0; i < kFlight; ++i) {
+      const int p = p0 + (kFlight + i) * kLanes;
+      if (p < parts) x[i] = __ldg(O + p * kStep);
+    }
+  }
+  sums[tid] = acc;
+  __syncthreads();
+  if (tid < kCols) {
+#pragma unroll
+    for (int i = 1; i < kLanes; ++i) {
+      const float4 v = sums[i * kCols + tid];
+      acc.x += v.x;
+      acc.y += v.y;
+      acc.z += v.z;
+      acc.w += v.w;
+    }
+    const float inv = sum == 0.f ? 0.f : 1.0f / sum;  // every part empty: 0
+    *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + static_cast<int64_t>(row) * D + tid * 4) =
+        make_uint2(pack2<T>(acc.x * inv, acc.y * inv), pack2<T>(acc.z * inv, acc.w * inv));
+    if (tid == 0 && a.lse != nullptr) a.lse[row] = sum == 0.f ? -INFINITY : top + __log2f(sum);
   }
 }
 

@@ -82,8 +82,8 @@ skv_status check_cache(const void* k, const void* v, const float* ks, const floa
   if (block < 1 || capacity % block != 0) return SKV_ERR_INVALID_ARG;
   if (D != 64 && D != 128 && D != 256) return SKV_ERR_UNSUPPORTED;
   if (block != 16 && block != 32 && block != 64 && block != 128) return SKV_ERR_UNSUPPORTED;
-  // 32-bit tile coordinates; capacity + a window stays in int
-  if (static_cast<int64_t>(B) * Hkv * capacity > (int64_t(1) << 31) - 1 || capacity > (1 << 30))
+  // 32-bit tile coordinates, also of tiles that reach behind the last token
+  if (static_cast<int64_t>(B) * Hkv * capacity > (int64_t(1) << 31) - 4096 || capacity > (1 << 30))
     return SKV_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(B) * Hkv > 65535) return SKV_ERR_UNSUPPORTED;  // grid.y
   return SKV_OK;
@@ -179,22 +179,48 @@ int launch_decode_kv8_d(const CUtensorMap& tk, const CUtensorMap& tv, const Kv8D
                   : launch_decode_kv8<D, T, false, false>(tk, tv, a, grid, st);
 }
 
+// keys of a tile of the division among CTAs
+int kv8_cta_keys(int D) {
+  return D == 64 ? Kv8DecodeCfg<64>::kCtaKeys : (D == 128 ? Kv8DecodeCfg<128>::kCtaKeys : Kv8DecodeCfg<256>::kCtaKeys);
+}
+
+int64_t kv8_units(int B, int Hq, int Hkv, int Lq) {
+  return static_cast<int64_t>(B) * Hkv * ceil_div64(static_cast<int64_t>(Hq / Hkv) * Lq, kKv8Rows);
+}
+
+// [B + 1] table | [slots, 16] LSE | [slots, 16, D] O where a unit can be
+// divided (slots: units + CTAs), then with weights [rows] LSE | [rows, capacity] logits
 struct Kv8Ws {
-  size_t part_o = 0, part_lse = 0, lse = 0, logits = 0, total = 0;
+  size_t table = 0, part_lse = 0, part_o = 0, lse = 0, logits = 0, total = 0;
+  bool divided = false;
 };
-Kv8Ws kv8_ws_layout(int B, int Hq, int Lq, int capacity, int D, int splits, int weights) {
+Kv8Ws kv8_ws_layout(int B, int Hq, int Hkv, int Lq, int capacity, int D, int ctas, int weights) {
   Kv8Ws w;
-  const size_t rows = static_cast<size_t>(B) * Hq * Lq;
-  if (splits > 1) {
-    w.part_lse = align256(static_cast<size_t>(splits) * rows * D * 4);
-    w.total = w.part_lse + align256(static_cast<size_t>(splits) * rows * 4);
+  auto take = [&](size_t bytes) {
+    const size_t at = w.total;
+    w.total += align256(bytes);
+    return at;
+  };
+  w.divided = ctas > 1 && capacity > kv8_cta_keys(D);
+  if (w.divided) {
+    const size_t slots = static_cast<size_t>(kv8_units(B, Hq, Hkv, Lq)) + ctas;
+    w.table = take((static_cast<size_t>(B) + 1) * 4);
+    w.part_lse = take(slots * kKv8Rows * 4);
+    w.part_o = take(slots * kKv8Rows * D * 4);
   }
   if (weights) {
-    w.lse = w.total;
-    w.logits = w.lse + align256(rows * 4);
-    w.total = w.logits + align256(rows * static_cast<size_t>(capacity) * 4);
+    const size_t rows = static_cast<size_t>(B) * Hq * Lq;
+    w.lse = take(rows * 4);
+    w.logits = take(rows * static_cast<size_t>(capacity) * 4);
   }
   return w;
+}
+
+template <typename T>
+int launch_kv8_merge(const Kv8DecodeArgs& a, int D, int ctas, unsigned rows, skv_stream_t st) {
+  if (D == 64) return launch(kv8_merge_kernel<64, T>, dim3(rows), 256, 0, st, 1, a, ctas);
+  if (D == 128) return launch(kv8_merge_kernel<128, T>, dim3(rows), 256, 0, st, 1, a, ctas);
+  return launch(kv8_merge_kernel<256, T>, dim3(rows), 256, 0, st, 1, a, ctas);
 }
 
 }  // namespace
@@ -377,53 +403,46 @@ skv_status kv8_fetch(const void* k_codes, const void* v_codes, const float* k_sc
 // ------------------------------------------------------------------ decode
 
 skv_status attn_splitkv_kv8_plan(int B, int Hq, int Hkv, int Lq, int capacity, int D, int num_sms,
-                                 int requested_splits, int* num_splits) {
-  if (num_splits == nullptr || B < 1 || Hq < 1 || Hkv < 1 || Lq < 1 || capacity < 1 || D < 1 || Hq % Hkv != 0)
+                                 int requested_ctas, int* num_ctas) {
+  if (num_ctas == nullptr || B < 1 || Hq < 1 || Hkv < 1 || Lq < 1 || capacity < 1 || D < 1 || Hq % Hkv != 0)
     return SKV_ERR_INVALID_ARG;
-  if (requested_splits < 0 || requested_splits > kSplitMax) return SKV_ERR_INVALID_ARG;
-  if (requested_splits > 0) {
-    *num_splits = requested_splits;
-    return SKV_OK;
-  }
-  if (num_sms < 1) return SKV_ERR_INVALID_ARG;
-  const int64_t units = static_cast<int64_t>(B) * Hkv * ceil_div64(static_cast<int64_t>(Hq / Hkv) * Lq, kKv8Rows);
-  int64_t s = std::max<int64_t>(1, 2 * static_cast<int64_t>(num_sms) / units);
-  s = std::min<int64_t>(s, ceil_div64(capacity, kSplitMinKeys));
-  s = std::min<int64_t>(s, kSplitMax);
-  const int64_t C = ceil_div64(ceil_div64(capacity, s), kSplitAlign) * kSplitAlign;
-  *num_splits = static_cast<int>(ceil_div64(capacity, C));
+  if (requested_ctas < 0 || requested_ctas > kKv8MaxCtas) return SKV_ERR_INVALID_ARG;
+  if (requested_ctas == 0 && num_sms < 1) return SKV_ERR_INVALID_ARG;
+  const int64_t places = kv8_units(B, Hq, Hkv, Lq) * (ceil_div64(capacity, kv8_cta_keys(D)) + 1);
+  const int64_t most = requested_ctas > 0 ? requested_ctas : std::min(2 * num_sms, kKv8MaxCtas);
+  *num_ctas = static_cast<int>(std::min(most, places));
   return SKV_OK;
 }
 
-size_t attn_splitkv_kv8_workspace(int B, int Hq, int Lq, int capacity, int D, int num_splits, int weights) {
-  if (B < 1 || Hq < 1 || Lq < 1 || capacity < 1 || D < 1 || num_splits < 1) return 0;
-  return kv8_ws_layout(B, Hq, Lq, capacity, D, num_splits, weights).total;
+size_t attn_splitkv_kv8_workspace(int B, int Hq, int Hkv, int Lq, int capacity, int D, int num_ctas, int weights) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Lq < 1 || capacity < 1 || D < 1 || num_ctas < 1) return 0;
+  return kv8_ws_layout(B, Hq, Hkv, Lq, capacity, D, num_ctas, weights).total;
 }
 
 skv_status attn_splitkv_decode_kv8(const void* q, const void* k_codes, const void* v_codes, const float* k_scale,
                                    const float* v_scale, void* out, float* lse, float* weights, int B, int Hq, int Hkv,
                                    int Lq, int capacity, int D, int block, float scale, skv_dtype dtype,
-                                   skv_code codes, const int32_t* kv_len, int causal, int num_splits, void* workspace,
+                                   skv_code codes, const int32_t* kv_len, int causal, int num_ctas, void* workspace,
                                    size_t workspace_bytes, skv_stream_t stream) {
   if (!good(q, 16) || !good(out, 16) || !aligned(lse, 4) || !aligned(weights, 16) || !aligned(kv_len, 4))
     return SKV_ERR_INVALID_ARG;
   if (Hq < 1 || Lq < 1 || Hkv < 1 || Hq % Hkv != 0) return SKV_ERR_INVALID_ARG;
   if (!(std::isfinite(scale) && scale > 0.f)) return SKV_ERR_INVALID_ARG;
   if (causal != 0 && causal != 1) return SKV_ERR_INVALID_ARG;
-  if (num_splits < 0 || num_splits > kSplitMax) return SKV_ERR_INVALID_ARG;
+  if (num_ctas < 0 || num_ctas > kKv8MaxCtas) return SKV_ERR_INVALID_ARG;
   if (skv_status s = check_cache(k_codes, v_codes, k_scale, v_scale, B, Hkv, capacity, D, block, codes)) return s;
   if (skv_status s = check_half(dtype)) return s;
   const int64_t group_rows = static_cast<int64_t>(Hq / Hkv) * Lq;
   const int64_t row_groups = ceil_div64(group_rows, kKv8Rows);
   const int64_t rows = static_cast<int64_t>(B) * Hq * Lq;
-  if (static_cast<int64_t>(B) * Hkv * row_groups > 65535 || rows > (1 << 30)) return SKV_ERR_UNSUPPORTED;
-  int splits = num_splits;
-  if (splits == 0) {
-    const int sms = sm_count();
-    if (sms <= 0) return cuda_status(cudaErrorNoDevice);
-    if (skv_status s = attn_splitkv_kv8_plan(B, Hq, Hkv, Lq, capacity, D, sms, 0, &splits)) return s;
-  }
-  const Kv8Ws w = kv8_ws_layout(B, Hq, Lq, capacity, D, splits, weights != nullptr);
+  // places of the division fit 32 bits
+  if (rows > (1 << 30) || kv8_units(B, Hq, Hkv, Lq) * (ceil_div64(capacity, kv8_cta_keys(D)) + 1) > 0x7fffffff)
+    return SKV_ERR_UNSUPPORTED;
+  const int sms = num_ctas == 0 ? sm_count() : 1;
+  if (sms <= 0) return cuda_status(cudaErrorNoDevice);
+  int ctas = 0;
+  if (skv_status s = attn_splitkv_kv8_plan(B, Hq, Hkv, Lq, capacity, D, sms, num_ctas, &ctas)) return s;
+  const Kv8Ws w = kv8_ws_layout(B, Hq, Hkv, Lq, capacity, D, ctas, weights != nullptr);
   if (workspace_bytes < w.total) return SKV_ERR_WORKSPACE_TOO_SMALL;
   if (w.total > 0 && !good(workspace, 256)) return SKV_ERR_INVALID_ARG;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -440,8 +459,9 @@ skv_status attn_splitkv_decode_kv8(const void* q, const void* k_codes, const voi
   a.q = q;
   a.out = out;
   a.lse = merged;
-  a.part_o = splits > 1 ? reinterpret_cast<float*>(ws + w.part_o) : nullptr;
-  a.part_lse = splits > 1 ? reinterpret_cast<float*>(ws + w.part_lse) : nullptr;
+  a.table = w.divided && kv_len != nullptr ? reinterpret_cast<uint32_t*>(ws + w.table) : nullptr;
+  a.part_o = w.divided ? reinterpret_cast<float*>(ws + w.part_o) : nullptr;
+  a.part_lse = w.divided ? reinterpret_cast<float*>(ws + w.part_lse) : nullptr;
   a.logits = weights != nullptr ? reinterpret_cast<float*>(ws + w.logits) : nullptr;
   a.k_scale = k_scale;
   a.v_scale = v_scale;
@@ -452,11 +472,10 @@ skv_status attn_splitkv_decode_kv8(const void* q, const void* k_codes, const voi
   a.Lq = Lq;
   a.capacity = capacity;
   a.block_shift = log2_of(block);
-  a.num_splits = splits;
   a.row_groups = static_cast<int>(row_groups);
   a.causal = causal;
   a.scale_log2 = scale * 1.4426950408889634f;
-  const dim3 grid(splits, static_cast<unsigned>(B * Hkv * row_groups));
+  const dim3 grid(static_cast<unsigned>(ctas));
   if (dtype == SKV_BF16) {
     if (D == 64) e = launch_decode_kv8_d<64, __nv_bfloat16>(tk, tv, a, codes, grid, stream);
     else if (D == 128) e = launch_decode_kv8_d<128, __nv_bfloat16>(tk, tv, a, codes, grid, stream);
@@ -467,9 +486,9 @@ skv_status attn_splitkv_decode_kv8(const void* q, const void* k_codes, const voi
     else e = launch_decode_kv8_d<256, __half>(tk, tv, a, codes, grid, stream);
   }
   if (e) return cuda_status(e);
-  if (splits > 1) {
-    e = launch_merge_state(a.part_o, a.part_lse, out, merged, splits, 1, 1, static_cast<int>(rows), D, 0, SKV_FP32,
-                           dtype, rows * D, rows, stream);
+  if (w.divided) {
+    e = dtype == SKV_BF16 ? launch_kv8_merge<__nv_bfloat16>(a, D, ctas, static_cast<unsigned>(rows), stream)
+                          : launch_kv8_merge<__half>(a, D, ctas, static_cast<unsigned>(rows), stream);
     if (e) return cuda_status(e);
   }
   if (weights != nullptr) {

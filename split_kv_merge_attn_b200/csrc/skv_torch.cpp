@@ -369,7 +369,7 @@ PyObject* py_kv8_fetch(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// decode_kv8(q, cache, scale, kv_len, causal, weights, num_splits, out, lse, return_lse, workspace, stream)
+// decode_kv8(q, cache, scale, kv_len, causal, weights, num_ctas, out, lse, return_lse, workspace, stream)
 PyObject* py_decode_kv8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 12, [&]() -> PyObject* {
     const at::Tensor& q = tensor(a[0], "q");
@@ -386,9 +386,9 @@ PyObject* py_decode_kv8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     auto* pw = static_cast<float*>(opt(a[5], "weights", bhn, at::kFloat, dev));
     const int iB = static_cast<int>(c.B), iHq = small(Hq, "Hq"), iHkv = static_cast<int>(c.Hkv), iLq = small(Lq, "Lq"),
               iN = static_cast<int>(c.capacity), iD = static_cast<int>(c.D);
-    int splits = integer(a[6], "num_splits");
+    int ctas = integer(a[6], "num_ctas");
     check(g_lib.plan(iB, iHq, iHkv, iLq, iN, iD, at::cuda::getDeviceProperties(static_cast<c10::DeviceIndex>(dev))->multiProcessorCount,
-                     splits, &splits),
+                     ctas, &ctas),
           "attn_splitkv_decode_kv8");
     at::Tensor out, lse, ws;
     void* po = opt(a[7], "out", shape, dt, dev);
@@ -410,7 +410,7 @@ PyObject* py_decode_kv8(PyObject*, PyObject* const* a, Py_ssize_t n) {
       pws = w.data_ptr();
       bytes = w.nbytes();
     } else {
-      bytes = g_lib.workspace(iB, iHq, iLq, iN, iD, splits, pw != nullptr);
+      bytes = g_lib.workspace(iB, iHq, iHkv, iLq, iN, iD, ctas, pw != nullptr);
       if (bytes > 0) {
         const int64_t size[1] = {static_cast<int64_t>(bytes)};
         ws = empty(size, at::kByte, dev);
@@ -420,7 +420,7 @@ PyObject* py_decode_kv8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const float scale = a[2] == Py_None ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(c.D))) : static_cast<float>(real(a[2]));
     const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
     check(g_lib.decode(pq, c.k, c.v, c.ks, c.vs, po, pl, pw, iB, iHq, iHkv, iLq, iN, iD, c.block, scale, code, c.code, pn,
-                       truth(a[4]), splits, pws, bytes, stream_of(a[11], dev)),
+                       truth(a[4]), ctas, pws, bytes, stream_of(a[11], dev)),
           "attn_splitkv_decode_kv8");
     return pair(result(a[7], out), want_lse ? result(a[8], lse) : Py_NewRef(Py_None));
   });

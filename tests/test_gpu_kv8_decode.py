@@ -75,18 +75,18 @@ def check(q, cache, out, lse, lengths, scale, causal, dtype, added=None):
         assert worst <= 0
 
 
-def run(B, Hq, Hkv, Lq, D, capacity, block, codes, dtype, lengths, causal=False, weights=False, splits=0, seed=0,
+def run(B, Hq, Hkv, Lq, D, capacity, block, codes, dtype, lengths, causal=False, weights=False, ctas=0, seed=0,
         q_mult=1.0, scale_span=1.0, full=False):
     cache = filled_cache(B, Hkv, capacity, D, block, codes, lengths, seed, scale_span)
     q = (torch.randn(B, Hq, Lq, D, generator=gen(seed + 1)) * q_mult).to(DT[dtype]).cuda()
     scale = D ** -0.5
-    ns = skv.attn_splitkv_kv8_plan(B, Hq, Hkv, Lq, capacity, D, 148, splits)
-    ws = torch.full((skv.attn_splitkv_kv8_workspace(B, Hq, Lq, capacity, D, ns, weights) + 1,), 0xFF, dtype=torch.uint8,
+    nc = skv.attn_splitkv_kv8_plan(B, Hq, Hkv, Lq, capacity, D, 148, ctas)
+    ws = torch.full((skv.attn_splitkv_kv8_workspace(B, Hq, Hkv, Lq, capacity, D, nc, weights) + 1,), 0xFF, dtype=torch.uint8,
                     device="cuda")  # NaN bit patterns
     out, lse = nan_empty(q.shape, q.dtype), nan_empty(q.shape[:3], torch.float32)
     w = torch.zeros(B, Hkv, capacity, device="cuda") if weights else None
     skv.attn_splitkv_decode_kv8(q, cache, scale, kv_len=None if full else i32(lengths), causal=causal, weights=w,
-                                num_splits=ns, out=out, lse=lse, workspace=ws)
+                                num_ctas=nc, out=out, lse=lse, workspace=ws)
     torch.cuda.synchronize()
     assert skv.device_error() == 0
     check(q, cache, out, lse, lengths, scale, causal, dtype, None if w is None else O.to_f64(w))
@@ -94,7 +94,7 @@ def run(B, Hq, Hkv, Lq, D, capacity, block, codes, dtype, lengths, causal=False,
 
 
 CASES = [
-    # B, Hq, Hkv, Lq, D, capacity, block, codes, dtype, lengths, causal, weights, splits
+    # B, Hq, Hkv, Lq, D, capacity, block, codes, dtype, lengths, causal, weights, ctas
     (1, 1, 1, 1, 64, 16, 16, "int8", "bf16", [1], False, True, 1),
     (1, 4, 4, 1, 128, 64, 64, "e4m3", "fp16", [17], False, True, 0),
     (2, 8, 2, 1, 128, 1024, 64, "int8", "bf16", [1000, 65], False, True, 0),
@@ -106,12 +106,21 @@ CASES = [
     (1, 16, 1, 1, 256, 128, 32, "int8", "fp16", [128], False, True, 1),
     (1, 32, 1, 1, 128, 256, 16, "int8", "bf16", [250], False, False, 4),       # 32 rows a kv head
     (4, 2, 2, 1, 128, 4096, 64, "int8", "fp16", [4096, 2049, 1, 4000], False, True, 0),
+    # the division among CTAs: shares that end inside units, hold several, or are empty
+    (5, 4, 2, 1, 64, 1536, 32, "int8", "bf16", [1536, 0, 257, 1, 900], False, True, 7),
+    (5, 4, 2, 1, 128, 1536, 32, "e4m3", "fp16", [0, 300, 0, 1200, 0], False, False, 5),
+    (2, 4, 4, 3, 256, 512, 64, "int8", "bf16", [512, 100], True, True, 37),
+    (130, 2, 1, 1, 64, 512, 16, "e4m3", "bf16", [(i * 37) % 513 for i in range(130)], False, False, 11),
+    (300, 1, 1, 1, 128, 272, 16, "int8", "fp16", [(i * 53) % 273 for i in range(300)], False, True, 0),
+    (2, 2, 1, 1, 64, 512, 16, "int8", "bf16", [0, 0], False, True, 4),
+    (1, 2, 1, 1, 128, 32768, 64, "e4m3", "bf16", [32768], False, False, 1024),
+    (1, 40, 1, 2, 128, 768, 64, "int8", "bf16", [700], True, True, 9),         # 80 rows: five row groups
 ]
 
 
-@pytest.mark.parametrize("B,Hq,Hkv,Lq,D,capacity,block,codes,dtype,lengths,causal,weights,splits", CASES)
-def test_against_oracle(B, Hq, Hkv, Lq, D, capacity, block, codes, dtype, lengths, causal, weights, splits):
-    run(B, Hq, Hkv, Lq, D, capacity, block, codes, dtype, lengths, causal, weights, splits, seed=capacity + D)
+@pytest.mark.parametrize("B,Hq,Hkv,Lq,D,capacity,block,codes,dtype,lengths,causal,weights,ctas", CASES)
+def test_against_oracle(B, Hq, Hkv, Lq, D, capacity, block, codes, dtype, lengths, causal, weights, ctas):
+    run(B, Hq, Hkv, Lq, D, capacity, block, codes, dtype, lengths, causal, weights, ctas, seed=capacity + D)
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
@@ -131,8 +140,8 @@ def test_workload_sizes():
 def test_silent_values_under_strong_logits(D):
     """A block of zero values (scale 0) with logits hundreds of log2 units above
     the rest, before and behind blocks with values: the output is 0, not NaN."""
-    B, Hkv, capacity, block = 1, 1, 256, 16
-    for strong in (0, 8, 15):
+    B, Hkv, capacity, block = 1, 1, 512, 16
+    for strong in (0, 8, 15, 31):
         cache = filled_cache(B, Hkv, capacity, D, block, "int8", [capacity], seed=3)
         q = torch.ones(B, 2, 1, D, dtype=torch.bfloat16, device="cuda")
         cache.k.fill_(-100)
@@ -140,8 +149,8 @@ def test_silent_values_under_strong_logits(D):
         cache.k[:, :, strong * 16: strong * 16 + 16] = 100
         cache.v[:, :, strong * 16: strong * 16 + 16] = 0
         cache.v_scale[:, :, strong] = 0.0
-        for splits in (1, 2):
-            out, lse = skv.attn_splitkv_decode_kv8(q, cache, 1.0, num_splits=splits)
+        for ctas in (1, 2):
+            out, lse = skv.attn_splitkv_decode_kv8(q, cache, 1.0, num_ctas=ctas)
             want = D * 100.0 * np.log2(np.e) + 4.0
             assert torch.all(out == 0), out.abs().max()
             assert np.all(np.abs(O.to_f64(lse) - want) <= 2.0 ** -22 * want + 2.0 ** -17)
@@ -153,14 +162,14 @@ def test_bad_scales_reach_only_rows_that_see_them(where, bad):
     """A non-finite scale (codes 0, as the append leaves them) makes the rows that
     see its block NaN; rows of other heads, and causal rows that end before the
     block, keep their values."""
-    B, Hq, Hkv, Lq, D, capacity, block, n = 1, 4, 2, 4, 128, 128, 16, 67
+    B, Hq, Hkv, Lq, D, capacity, block, n = 1, 4, 2, 4, 128, 512, 16, 323
     cache = filled_cache(B, Hkv, capacity, D, block, "int8", [n], seed=9)
     q = torch.randn(B, Hq, Lq, D, generator=gen(2)).bfloat16().cuda()
     ref, lref = skv.attn_splitkv_decode_kv8(q, cache, kv_len=i32([n]), causal=True)
-    getattr(cache, where)[0, 0, 4] = bad             # keys 64..66 of head 0: rows 1..3 see some of them
-    (cache.k if where == "k_scale" else cache.v)[0, 0, 64:80] = 0
-    for splits in (1, 2):
-        out, lse = skv.attn_splitkv_decode_kv8(q, cache, kv_len=i32([n]), causal=True, num_splits=splits)
+    getattr(cache, where)[0, 0, 20] = bad            # keys 320..322 of head 0: rows 1..3 see some of them
+    (cache.k if where == "k_scale" else cache.v)[0, 0, 320:336] = 0
+    for ctas in (1, 2):
+        out, lse = skv.attn_splitkv_decode_kv8(q, cache, kv_len=i32([n]), causal=True, num_ctas=ctas)
         assert torch.isnan(out[:, :2, 1:]).all()
         assert torch.isnan(lse[:, :2, 1:]).all() or where == "v_scale"
         assert torch.isfinite(out[:, :2, 0]).all() and torch.isfinite(out[:, 2:]).all()
@@ -169,11 +178,11 @@ def test_bad_scales_reach_only_rows_that_see_them(where, bad):
 
 
 def test_bad_queries_give_nan():
-    cache = filled_cache(1, 1, 256, 64, 16, "int8", [256], seed=1)
+    cache = filled_cache(1, 1, 512, 64, 16, "int8", [512], seed=1)
     q = torch.ones(1, 2, 1, 64, dtype=torch.bfloat16, device="cuda")
     q[0, 1, 0, 5] = float("nan")
-    for splits in (1, 2):
-        out, lse = skv.attn_splitkv_decode_kv8(q, cache, num_splits=splits)
+    for ctas in (1, 2):
+        out, lse = skv.attn_splitkv_decode_kv8(q, cache, num_ctas=ctas)
         assert torch.isfinite(out[0, 0]).all() and torch.isnan(out[0, 1]).all() and torch.isnan(lse[0, 1]).all()
 
 
@@ -219,15 +228,15 @@ def test_graphs_follow_kv_len_and_contents():
     cache = filled_cache(B, Hkv, capacity, D, 64, "int8", [capacity] * B, seed=8)
     q = torch.zeros(B, Hq, 1, D, dtype=torch.bfloat16, device="cuda")
     kv_len = i32([5, 5])
-    ns = skv.attn_splitkv_kv8_plan(B, Hq, Hkv, 1, capacity, D)
-    nbytes = skv.attn_splitkv_kv8_workspace(B, Hq, 1, capacity, D, ns, True)
+    nc = skv.attn_splitkv_kv8_plan(B, Hq, Hkv, 1, capacity, D)
+    nbytes = skv.attn_splitkv_kv8_workspace(B, Hq, Hkv, 1, capacity, D, nc, True)
     sets = []
     for _ in range(2):
         ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
         w = torch.zeros(B, Hkv, capacity, device="cuda")
         out, lse = torch.empty_like(q), torch.empty(B, Hq, 1, device="cuda")
         call = lambda ws=ws, w=w, out=out, lse=lse: skv.attn_splitkv_decode_kv8(  # noqa: E731
-            q, cache, kv_len=kv_len, weights=w, out=out, lse=lse, workspace=ws, num_splits=ns)
+            q, cache, kv_len=kv_len, weights=w, out=out, lse=lse, workspace=ws, num_ctas=nc)
         call()
         torch.cuda.synchronize()
         graph = torch.cuda.CUDAGraph()

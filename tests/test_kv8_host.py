@@ -76,7 +76,7 @@ def fetch(**kw):
 
 def decode(**kw):
     a = dict(q=addr(8), **CACHE, out=addr(9), lse=None, w=None, B=2, Hq=4, Hkv=2, Lq=1, cap=128, D=128, block=32,
-             scale=0.1, dt=0, codes=0, kv_len=None, causal=0, splits=1, ws=None, wsb=0)
+             scale=0.1, dt=0, codes=0, kv_len=None, causal=0, ctas=1, ws=None, wsb=0)
     a.update(kw)
     return skv.lib().attn_splitkv_decode_kv8(*a.values(), None)
 
@@ -126,10 +126,10 @@ def test_fetch_refusals(status, kw):
 @pytest.mark.parametrize("status,kw", [
     (INVALID, dict(q=None)), (INVALID, dict(out=None)), (INVALID, dict(lse=addr(5) + 2)), (INVALID, dict(w=addr(5) + 4)),
     (INVALID, dict(kv_len=addr(5) + 2)), (INVALID, dict(Hq=3)), (INVALID, dict(Hq=0)), (INVALID, dict(Lq=0)),
-    (INVALID, dict(scale=0.0)), (INVALID, dict(scale=math.nan)), (INVALID, dict(causal=2)), (INVALID, dict(splits=-1)),
-    (INVALID, dict(splits=257)), (UNSUPPORTED, dict(dt=2)), (INVALID, dict(dt=-1)),
-    (UNSUPPORTED, dict(Hq=2 * 16 * 20000)), (WS_SMALL, dict(splits=2)), (WS_SMALL, dict(w=addr(5))),
-    (INVALID, dict(w=addr(5), wsb=1 << 30)), (INVALID, dict(splits=2, ws=P + 16, wsb=1 << 30)),
+    (INVALID, dict(scale=0.0)), (INVALID, dict(scale=math.nan)), (INVALID, dict(causal=2)), (INVALID, dict(ctas=-1)),
+    (INVALID, dict(ctas=1025)), (UNSUPPORTED, dict(dt=2)), (INVALID, dict(dt=-1)),
+    (UNSUPPORTED, dict(Hq=1 << 29, Lq=8)), (WS_SMALL, dict(ctas=2, cap=512)), (WS_SMALL, dict(w=addr(5))),
+    (INVALID, dict(w=addr(5), wsb=1 << 30)), (INVALID, dict(ctas=2, cap=512, ws=P + 16, wsb=1 << 30)),
 ])
 def test_decode_refusals(status, kw):
     assert decode(**kw) == status
@@ -149,21 +149,21 @@ def test_evict_refusals(status, kw):
 
 def test_workspace_and_plan():
     a = lambda x: (x + 255) // 256 * 256  # noqa: E731
-    for B, Hq, Lq, cap, D, s, w in [(1, 32, 1, 4096, 128, 16, 0), (2, 8, 3, 320, 64, 1, 1), (1, 4, 1, 64, 256, 1, 0),
-                                    (3, 6, 2, 1024, 256, 5, 1)]:
-        rows = B * Hq * Lq
-        want = (a(s * rows * D * 4) + a(s * rows * 4) if s > 1 else 0) + (a(rows * 4) + a(rows * cap * 4) if w else 0)
-        assert skv.attn_splitkv_kv8_workspace(B, Hq, Lq, cap, D, s, bool(w)) == want
-    assert skv.attn_splitkv_kv8_workspace(1, 4, 1, 64, 128, 0) == 0
-    rng = np.random.default_rng(0)
-    for _ in range(200):
-        hkv, g = int(rng.integers(1, 17)), int(rng.integers(1, 9))
-        B, Lq, cap = int(rng.integers(1, 33)), int(rng.integers(1, 9)), 16 * int(rng.integers(1, 9000))
-        s = skv.attn_splitkv_kv8_plan(B, hkv * g, hkv, Lq, cap, 128, int(rng.integers(1, 200)))
-        assert 1 <= s <= 256
-        per = 64 * -(-(-(-cap // s)) // 64)
-        assert (s - 1) * per < cap <= s * per  # no split is empty at the full capacity
-    for bad in [dict(B=0), dict(Hq=5, Hkv=2), dict(capacity=0), dict(num_sms=0), dict(requested_splits=257)]:
+    for B, Hq, Hkv, Lq, cap, D, c, w in [(1, 32, 8, 1, 4096, 128, 16, 0), (2, 8, 2, 3, 320, 64, 1, 1),
+                                         (1, 4, 4, 1, 64, 256, 3, 0), (3, 6, 1, 5, 1024, 256, 5, 1),
+                                         (2, 4, 2, 1, 256, 128, 4, 0)]:
+        rows, units = B * Hq * Lq, B * Hkv * -(-Hq // Hkv * Lq // 16)
+        slots = 16 * (units + c)
+        divided = c > 1 and cap > (64 if D == 256 else 256)
+        want = a(4 * (B + 1)) + a(4 * slots) + a(4 * slots * D) if divided else 0
+        want += a(4 * rows) + a(4 * rows * cap) if w else 0
+        assert skv.attn_splitkv_kv8_workspace(B, Hq, Hkv, Lq, cap, D, c, bool(w)) == want
+    assert skv.attn_splitkv_kv8_workspace(1, 4, 4, 1, 64, 128, 0) == 0
+    assert skv.attn_splitkv_kv8_plan(1, 32, 8, 1, 4096) == 8 * 17   # a place for each tile of 256 keys and one more
+    assert skv.attn_splitkv_kv8_plan(1, 32, 8, 1, 32768) == 296
+    assert skv.attn_splitkv_kv8_plan(1, 16, 4, 1, 4096, 256) == 4 * 65
+    assert skv.attn_splitkv_kv8_plan(1, 32, 8, 1, 4096, requested_ctas=7) == 7
+    for bad in [dict(B=0), dict(Hq=5, Hkv=2), dict(capacity=0), dict(num_sms=0), dict(requested_ctas=1025)]:
         with pytest.raises(skv.SkvError):
             skv.attn_splitkv_kv8_plan(**{**dict(B=1, Hq=4, Hkv=2, Lq=1, capacity=64), **bad})
 
