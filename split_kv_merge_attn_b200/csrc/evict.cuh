@@ -22,7 +22,7 @@ namespace skv {
 constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kEvictBins = 256;
-constexpr int kEvictChunk = 8;  // keys a lane holds
+constexpr int kEvictChunk = 16;  // keys a lane holds
 
 struct EvictArgs {
   const float* weights;      // [B, Hkv, capacity]
@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const Evict
   const int wanted = a.budget - a.sink - a.recent;
   const float* w = a.weights + bh * a.capacity;
 
-  // this CTA's candidates, and this warp's (in order), in chunks of 256 to a warp
+  // this CTA's candidates, and this warp's (in order), in chunks of 512 to a warp
   const int per_cta = ((hi - lo + static_cast<int>(parts) - 1) / static_cast<int>(parts) + 31) / 32 * 32;
   const int c0 = min(lo + static_cast<int>(rank) * per_cta, hi), c1 = min(c0 + per_cta, hi);
   const int per_warp = ((c1 - c0 + kEvictWarps - 1) / kEvictWarps + 31) / 32 * 32;
@@ -139,9 +139,10 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const Evict
       }
       cluster_barrier();
       if (tid < kEvictBins) {
-        uint32_t t = 0;
-        for (uint32_t r = 0; r < parts; ++r) t += ld_cluster_u32(&sums[pass][tid], r);
-        all[tid] = t;
+        uint32_t t[8];  // all requested before the first is used
+#pragma unroll
+        for (uint32_t r = 0; r < 8; ++r) t[r] = r < parts ? ld_cluster_u32(&sums[pass][tid], r) : 0u;
+        all[tid] = ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
       }
       __syncthreads();
       if (warp == 0) {
@@ -203,9 +204,12 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const Evict
   }
   cluster_barrier();
   uint32_t place = 0, seen = 0;  // candidates above / equal before this warp's
-  for (uint32_t r = 0; r < rank; ++r) {
-    place += ld_cluster_u32(&counts[0], r);
-    seen += ld_cluster_u32(&counts[1], r);
+#pragma unroll
+  for (uint32_t r = 0; r < 7; ++r) {
+    if (r < rank) {
+      place += ld_cluster_u32(&counts[0], r);
+      seen += ld_cluster_u32(&counts[1], r);
+    }
   }
   cluster_barrier();  // nobody leaves while its counts or histograms may be read
   for (int i = 0; i < warp; ++i) {

@@ -12,9 +12,9 @@
 // themselves are always finite.
 //
 // Bound by bytes (16 bits in, 8 out).  One CTA takes 128 tokens of one
-// (batch entry, head) of K or of V, each of its 8 warps 16 of them, which it
-// holds in registers between the maximum and the codes: one read, one write.
-// Every block size (16, 32, 64, 128) is then a whole number of warps.
+// (batch entry, head) of K or of V, each of its warps 16 of them (8 at D = 256),
+// which it holds in registers between the maximum and the codes: one read, one
+// write.  Every block size (16, 32, 64, 128) is then a whole number of warps.
 #pragma once
 
 #include "skv_device.cuh"
@@ -22,6 +22,8 @@
 namespace skv {
 
 constexpr int kKv8Window = 128;   // tokens per append CTA
+template <int D>
+constexpr int kAppendThreads = D == 256 ? 512 : 256;
 constexpr float kKv8TinyScale = 1.17549435e-38f;  // 2^-126
 
 template <bool kE4M3>
@@ -90,11 +92,13 @@ struct Kv8AppendArgs {
 };
 
 template <int D, typename T, bool kE4M3>
-__global__ void __launch_bounds__(256, D == 64 ? 5 : (D == 128 ? 4 : 2)) kv8_append_kernel(const Kv8AppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads<D>, D == 64 ? 5 : (D == 128 ? 4 : 2)) kv8_append_kernel(const Kv8AppendArgs a) {
   using Code = Kv8Code<kE4M3>;
   constexpr int kLanes = D / 8;            // lanes of one row, 8 values each
   constexpr int kRows = 32 / kLanes;       // rows a warp takes at once
-  constexpr int kPasses = 16 / kRows;
+  constexpr int kWarps = kAppendThreads<D> / 32;
+  constexpr int kTokens = kKv8Window / kWarps;  // of a warp
+  constexpr int kPasses = kTokens / kRows;
   // a programmatic dependent of the kernel before it: waits before any load
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -115,14 +119,16 @@ __global__ void __launch_bounds__(256, D == 64 ? 5 : (D == 128 ? 4 : 2)) kv8_app
   if (base >= end || start >= end) return;  // the whole CTA: nothing new in this window
 
   const int cl = lane % kLanes, rl = lane / kLanes;
-  const int wpos = base + warp * 16;       // this warp's first position
+  const int wpos = base + warp * kTokens;  // this warp's first position
   const int pos0 = wpos + rl;              // this lane's rows: pos0 + kRows * p
-  const int per = a.block >> 4;            // warps of one block
+  const int per = a.block / kTokens;       // warps of one block
   const int group = warp / per;
   const int block_pos = base + group * a.block;
   const bool touched = block_pos < end && block_pos + a.block > start;
   const bool has_old = touched && block_pos < start;  // older tokens, with a scale of their own
-  const bool whole = wpos >= start && wpos + 16 <= end;  // new rows only
+  const bool whole = wpos >= start && wpos + kTokens <= end;  // new rows only
+  const int64_t at = (static_cast<int64_t>(b) * a.Hkv + h) * (a.capacity / a.block) + block_pos / a.block;
+  const float s_old = has_old ? a.scale[which][at] : 0.f;
   // rows of token i: row0 + i * step
   const int64_t step = (a.cu != nullptr || a.token_major) ? a.Hkv : 1;
   const int64_t row0 = a.cu != nullptr ? static_cast<int64_t>(first_row) * a.Hkv + h
@@ -160,9 +166,7 @@ __global__ void __launch_bounds__(256, D == 64 ? 5 : (D == 128 ? 4 : 2)) kv8_app
   }
   top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
 
-  __shared__ uint32_t warp_top[8];
-  const int64_t at = (static_cast<int64_t>(b) * a.Hkv + h) * (a.capacity / a.block) + block_pos / a.block;
-  const float s_old = has_old ? a.scale[which][at] : 0.f;
+  __shared__ uint32_t warp_top[kWarps];
   if (lane == 0) warp_top[warp] = top;
   __syncthreads();  // also orders every read of the old scale before its new value is written
   if (!touched) return;
@@ -213,11 +217,11 @@ struct Kv8FetchArgs {
   int token_major;         // out [B, n, Hkv, D] instead of [B, Hkv, n, D]
 };
 
-constexpr int kFetchUnroll = 4;  // 16-code pieces a thread has in flight
+constexpr int kFetchUnroll = 8;  // pieces of 8 codes a thread has in flight (each a full 16 bytes out)
 
 template <int D, typename T, bool kE4M3>
 __global__ void __launch_bounds__(256) kv8_fetch_kernel(const Kv8FetchArgs a) {
-  constexpr int kUnits = D / 16;
+  constexpr int kUnits = D / 8;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int bh = blockIdx.y, which = blockIdx.z;
@@ -229,37 +233,36 @@ __global__ void __launch_bounds__(256) kv8_fetch_kernel(const Kv8FetchArgs a) {
   T* out = static_cast<T*>(a.out[which]);
   constexpr int kRowsCta = 256 * kFetchUnroll / kUnits;
   const int i0 = blockIdx.x * kRowsCta + threadIdx.x / kUnits, u = threadIdx.x % kUnits;
-  uint4 w[kFetchUnroll];
+  uint2 w[kFetchUnroll];
   float s[kFetchUnroll];
 #pragma unroll
   for (int j = 0; j < kFetchUnroll; ++j) {
     const int i = i0 + j * (256 / kUnits);
     const int64_t pos = start + i;
-    w[j] = make_uint4(0, 0, 0, 0);
-    s[j] = 0.f;  // a position without a token: zeros (e4m3 and, below, int8 codes 0)
+    w[j] = make_uint2(0, 0);
+    s[j] = 0.f;  // a position without a token: zeros
     if (i < a.n && pos >= 0 && pos < len) {
-      w[j] = __ldg(reinterpret_cast<const uint4*>(codes + pos * D) + u);
+      w[j] = __ldg(reinterpret_cast<const uint2*>(codes + pos * D) + u);
       s[j] = __ldg(scale + (pos >> a.block_shift));
     }
   }
+  const int64_t row0 = a.token_major ? static_cast<int64_t>(b) * a.n * a.Hkv + h : static_cast<int64_t>(bh) * a.n;
+  const int64_t step = a.token_major ? a.Hkv : 1;
 #pragma unroll
   for (int j = 0; j < kFetchUnroll; ++j) {
     const int i = i0 + j * (256 / kUnits);
     if (i >= a.n) break;
-    const uint32_t in[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
-    uint32_t o[8];
+    const uint64_t ss = f2_pack(s[j], s[j]);
+    uint32_t o[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < 2; ++e) {
       float x[4];
-      Kv8Code<kE4M3>::decode4(in[e], x);
-      o[2 * e] = pack2<T>(x[0] * s[j], x[1] * s[j]);
-      o[2 * e + 1] = pack2<T>(x[2] * s[j], x[3] * s[j]);
+      Kv8Code<kE4M3>::decode4(e ? w[j].y : w[j].x, x);
+      const float2 p = f2_unpack(fmul2(f2_pack(x[0], x[1]), ss)), q = f2_unpack(fmul2(f2_pack(x[2], x[3]), ss));
+      o[2 * e] = pack2<T>(p.x, p.y);
+      o[2 * e + 1] = pack2<T>(q.x, q.y);
     }
-    const int64_t row = a.token_major ? (static_cast<int64_t>(b) * a.n + i) * a.Hkv + h
-                                      : static_cast<int64_t>(bh) * a.n + i;
-    uint4* dst = reinterpret_cast<uint4*>(out + row * D) + 2 * u;
-    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    reinterpret_cast<uint4*>(out + (row0 + i * step) * D)[u] = make_uint4(o[0], o[1], o[2], o[3]);
   }
 }
 

@@ -12,9 +12,10 @@
 // (off by 2^-25 turns).  The values turn in fp32 and are rounded once.
 //
 // Bound by bytes: each value is read and written once.  A thread has one unit of
-// 8 pairs (two 16-byte pieces) of one head, and takes it through the CTA's tokens;
-// the CTA's sines and cosines are computed once, into shared memory, while the
-// values are on their way.
+// 8 pairs, two 16-byte pieces half a rotary dimension apart (in either layout of
+// pairs: neighbouring threads then fill whole sectors), of one head, and takes it
+// through the CTA's tokens; the CTA's sines and cosines are computed once, into
+// shared memory, while the values are on their way.
 #pragma once
 
 #include "skv_device.cuh"
@@ -51,16 +52,16 @@ __global__ void __launch_bounds__(kRopeMaxThreads, 2) rope_kernel(const RopeArgs
   const int head = blockIdx.y * a.group + hh;  // q's heads, then k's
   const int which = head >= a.heads[0] ? 1 : 0;
   const int h = head - (which ? a.heads[0] : 0), H = a.heads[which];
-  const bool turns = u * 16 < a.R;
-  const bool split = turns && !kInterleaved;   // pieces half a rotary dimension apart
-  const int gap = split ? half : 8;
+  const int turning = a.R >> 4;                // units of pairs; the others are copied
+  const bool turns = u < turning;
+  const int gap = turns ? half : (a.D - a.R) >> 1;
   const T* src = static_cast<const T*>(a.x[which]);
   T* dst = static_cast<T*>(a.y[which]);
   const bool mine = hh < a.group && head < a.heads[0] + a.heads[1] && (turns || src != dst);
 
   // element offset of the unit in each token
   int64_t at[kRopeTokens];
-  const int d = split ? u * 8 : u * 16;
+  const int d = turns ? u * 8 : a.R + (u - turning) * 8;
   if (a.token_major) {
 #pragma unroll
     for (int i = 0; i < kRopeTokens; ++i) at[i] = (static_cast<int64_t>(t0 + i) * H + h) * a.D + d;
@@ -87,7 +88,11 @@ __global__ void __launch_bounds__(kRopeMaxThreads, 2) rope_kernel(const RopeArgs
     }
   }
   for (int i = threadIdx.x; i < nt * half; i += blockDim.x) {
-    const int tt = i / half, pair = i - tt * half;
+    // entry i is the one of (token, quarter e, unit, lower or upper pair of the
+    // quarter): a quarter's entries lie side by side for neighbouring units
+    const int tt = i / half, j = i - tt * half;
+    const int e = j / (2 * turning), in = j - e * 2 * turning, unit = in >> 1, up = in & 1;
+    const int pair = kInterleaved ? (e >> 1) * (half >> 1) + unit * 4 + (e & 1) * 2 + up : unit * 8 + e * 2 + up;
     const double t = static_cast<double>(a.pos[t0 + tt]) * (a.inverse ? -0.15915494309189535 : 0.15915494309189535) *
                      a.inv_freq[pair];  // turns
     float c, s;
@@ -102,18 +107,19 @@ __global__ void __launch_bounds__(kRopeMaxThreads, 2) rope_kernel(const RopeArgs
     uint32_t w0[4] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w};
     uint32_t w1[4] = {v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
     if (turns) {
-      const float4* cs = reinterpret_cast<const float4*>(table + i * half + u * 8);  // two pairs each
+      const float4* cs = reinterpret_cast<const float4*>(table + i * half) + u;  // quarter e: cs[e * turning]
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float2 f0 = unpack2<T>(w0[e]), f1 = unpack2<T>(w1[e]);
+        const float4 t = cs[e * turning];  // (cos, sin) of two pairs
         if constexpr (kInterleaved) {
-          const float4 ta = cs[e >> 1], tb = cs[2 + (e >> 1)];
-          const float ca = e & 1 ? ta.z : ta.x, sa = e & 1 ? ta.w : ta.y;
-          const float cb = e & 1 ? tb.z : tb.x, sb = e & 1 ? tb.w : tb.y;
-          w0[e] = pack2<T>(f0.x * ca - f0.y * sa, f0.x * sa + f0.y * ca);
-          w1[e] = pack2<T>(f1.x * cb - f1.y * sb, f1.x * sb + f1.y * cb);
+          // quarters 0 and 1 are words of the first piece, 2 and 3 of the second
+          uint32_t& wa = e < 2 ? w0[2 * e] : w1[2 * e - 4];
+          uint32_t& wb = e < 2 ? w0[2 * e + 1] : w1[2 * e - 3];
+          const float2 fa = unpack2<T>(wa), fb = unpack2<T>(wb);
+          wa = pack2<T>(fa.x * t.x - fa.y * t.y, fa.x * t.y + fa.y * t.x);
+          wb = pack2<T>(fb.x * t.z - fb.y * t.w, fb.x * t.w + fb.y * t.z);
         } else {
-          const float4 t = cs[e];
+          const float2 f0 = unpack2<T>(w0[e]), f1 = unpack2<T>(w1[e]);
           w0[e] = pack2<T>(f0.x * t.x - f1.x * t.y, f0.y * t.z - f1.y * t.w);
           w1[e] = pack2<T>(f0.x * t.y + f1.x * t.x, f0.y * t.w + f1.y * t.z);
         }

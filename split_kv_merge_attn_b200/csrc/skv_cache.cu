@@ -98,8 +98,8 @@ int log2_of(int block) { return block == 16 ? 4 : (block == 32 ? 5 : (block == 6
 
 template <int D, typename T>
 int launch_append(const Kv8AppendArgs& a, skv_code codes, dim3 grid, skv_stream_t st) {
-  return codes == SKV_E4M3 ? launch(kv8_append_kernel<D, T, true>, grid, 256, 0, st, 1, a)
-                           : launch(kv8_append_kernel<D, T, false>, grid, 256, 0, st, 1, a);
+  return codes == SKV_E4M3 ? launch(kv8_append_kernel<D, T, true>, grid, kAppendThreads<D>, 0, st, 1, a)
+                           : launch(kv8_append_kernel<D, T, false>, grid, kAppendThreads<D>, 0, st, 1, a);
 }
 
 template <typename T>
@@ -111,7 +111,7 @@ int launch_append_d(const Kv8AppendArgs& a, int D, skv_code codes, dim3 grid, sk
 
 template <int D, typename T>
 int launch_fetch(const Kv8FetchArgs& a, int B, skv_code codes, skv_stream_t st) {
-  const dim3 grid(static_cast<unsigned>(ceil_div64(a.n, 256 * kFetchUnroll / (D / 16))),
+  const dim3 grid(static_cast<unsigned>(ceil_div64(a.n, 256 * kFetchUnroll / (D / 8))),
                   static_cast<unsigned>(B * a.Hkv), 2);
   return codes == SKV_E4M3 ? launch(kv8_fetch_kernel<D, T, true>, grid, 256, 0, st, 1, a)
                            : launch(kv8_fetch_kernel<D, T, false>, grid, 256, 0, st, 1, a);
@@ -557,9 +557,13 @@ skv_status kv8_evict(const void* k_codes, const void* v_codes, const float* k_sc
   a.budget = budget;
   a.sink = sink;
   a.recent = recent;
-  // about 4096 tokens a CTA, at most 8 CTAs a cluster
+  // 4096 tokens a CTA, or 8192 (all a warp's keys still in registers) where that
+  // many CTAs would not be resident at once; at most 8 CTAs a cluster
+  const int sms = sm_count();
+  if (sms <= 0) return cuda_status(cudaErrorNoDevice);
+  const int64_t each = static_cast<int64_t>(B) * Hkv * ceil_div64(capacity, 4096) > 2 * sms ? 8192 : 4096;
   unsigned cluster = 1;
-  while (cluster < 8 && static_cast<int64_t>(cluster) * 4096 < capacity) cluster *= 2;
+  while (cluster < 8 && cluster * each < capacity) cluster *= 2;
   int e = launch(evict_select_kernel, dim3(cluster, static_cast<unsigned>(B * Hkv)), kEvictThreads, 0, stream, cluster, a);
   if (e) return cuda_status(e);
   const int64_t most = std::min(budget, capacity);
