@@ -914,6 +914,11 @@ __global__ void __launch_bounds__(256) kv8_weights_kernel(const Kv8WeightArgs a)
   if (j >= n) return;
   const float* x = a.logits + bh * a.rows * a.capacity + j;
   const float* lse = a.lse + bh * a.rows;
+  // what is there already, requested first
+  float* w = a.weights + bh * a.capacity + j;
+  const bool four = j + 4 <= n;
+  float4 old = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (four) old = *reinterpret_cast<const float4*>(w);
   float s[4] = {0.f, 0.f, 0.f, 0.f};
   // eight rows in flight
   for (int r0 = 0; r0 < a.rows; r0 += 8) {
@@ -934,11 +939,8 @@ __global__ void __launch_bounds__(256) kv8_weights_kernel(const Kv8WeightArgs a)
       s[3] += ex2_approx(v[i].w - L[i]);
     }
   }
-  float* w = a.weights + bh * a.capacity + j;
-  if (j + 4 <= n) {
-    float4 v = *reinterpret_cast<float4*>(w);
-    v.x += s[0]; v.y += s[1]; v.z += s[2]; v.w += s[3];
-    *reinterpret_cast<float4*>(w) = v;
+  if (four) {
+    *reinterpret_cast<float4*>(w) = make_float4(old.x + s[0], old.y + s[1], old.z + s[2], old.w + s[3]);
   } else {
 #pragma unroll
     for (int e = 0; e < 4; ++e)

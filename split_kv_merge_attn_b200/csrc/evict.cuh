@@ -8,10 +8,15 @@
 // a token whose scale is the block's keeps its codes.
 //
 // Selection: weights map to whole numbers of the same order (NaN below all,
-// -0 equal to +0) and the threshold is found 8 bits at a time: a histogram of
-// the candidates that share the bits found so far, then the bin in which the
-// wanted rank falls.  A head's tokens are divided over the CTAs of a cluster,
-// which add up their histograms through distributed shared memory.
+// -0 equal to +0) and the threshold is found 11, 11 and 10 bits at a time: a
+// histogram of the candidates that share the bits found so far, then the bin in
+// which the wanted rank falls.  (8 bits at a time took four such rounds, and had
+// more lanes meet at a bin: weights of a head share few exponents.)  A head's
+// tokens are divided over the CTAs of a cluster, which add what their bins hold to
+// those of the first through distributed shared memory; that one finds the bin
+// and tells the others.  (Every CTA reading all the others' bins instead moved 64 KB
+// a round and CTA: 3.5 us a round against 0.9 us for a head of one CTA.)  Bound by
+// the rounds' latency: a head's weights are a few bytes per clock.
 #pragma once
 
 #include "skv_device.cuh"
@@ -21,8 +26,7 @@ namespace skv {
 
 constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
-constexpr int kEvictBins = 256;
-constexpr int kEvictChunk = 16;  // keys a lane holds
+constexpr int kEvictBins = 2048;
 
 struct EvictArgs {
   const float* weights;      // [B, Hkv, capacity]
@@ -54,17 +58,28 @@ __device__ __forceinline__ uint32_t cluster_nctarank() {
   return r;
 }
 __device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
-// a 32-bit word of another CTA of the cluster, at the same shared address as `local`
-__device__ __forceinline__ uint32_t ld_cluster_u32(const uint32_t* local, uint32_t rank) {
-  uint32_t addr, v;
+// words of another CTA of the cluster, at the same shared address as `local`
+__device__ __forceinline__ uint32_t cluster_address(const void* local, uint32_t rank) {
+  uint32_t addr;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(local)), "r"(rank));
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return addr;
+}
+__device__ __forceinline__ uint32_t ld_cluster_u32(const uint32_t* local, uint32_t rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_address(local, rank)) : "memory");
   return v;
 }
+__device__ __forceinline__ void add_cluster_u32(const uint32_t* local, uint32_t rank, uint32_t v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(cluster_address(local, rank)), "r"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster_u32(const uint32_t* local, uint32_t rank, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_address(local, rank)), "r"(v) : "memory");
+}
 
-// One cluster per (batch entry, head).
+// One cluster per (batch entry, head); a lane holds up to kChunk keys at a time.
+template <int kChunk>
 __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const EvictArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -87,104 +102,108 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const Evict
   const int wanted = a.budget - a.sink - a.recent;
   const float* w = a.weights + bh * a.capacity;
 
-  // this CTA's candidates, and this warp's (in order), in chunks of 512 to a warp
+  // this CTA's candidates, and this warp's (in order), in chunks of 32 * kChunk to a warp
   const int per_cta = ((hi - lo + static_cast<int>(parts) - 1) / static_cast<int>(parts) + 31) / 32 * 32;
   const int c0 = min(lo + static_cast<int>(rank) * per_cta, hi), c1 = min(c0 + per_cta, hi);
   const int per_warp = ((c1 - c0 + kEvictWarps - 1) / kEvictWarps + 31) / 32 * 32;
   const int w0 = min(c0 + warp * per_warp, c1), w1 = min(w0 + per_warp, c1);
   // keys j, j + 32, ... of a chunk in a lane; 0 (below every weight's) behind the
   // end, where NaN is 1.  A warp of one chunk keeps it in registers.
-  uint32_t key[kEvictChunk];
+  uint32_t key[kChunk];
   auto load = [&](int j) {
-    float x[kEvictChunk];
+    float x[kChunk];
 #pragma unroll
-    for (int i = 0; i < kEvictChunk; ++i) x[i] = j + 32 * i + lane < w1 ? __ldg(w + j + 32 * i + lane) : 0.f;
+    for (int i = 0; i < kChunk; ++i) x[i] = j + 32 * i + lane < w1 ? __ldg(w + j + 32 * i + lane) : 0.f;
 #pragma unroll
-    for (int i = 0; i < kEvictChunk; ++i) key[i] = j + 32 * i + lane < w1 ? weight_key(x[i]) : 0u;
+    for (int i = 0; i < kChunk; ++i) key[i] = j + 32 * i + lane < w1 ? weight_key(x[i]) : 0u;
   };
-  const bool one_chunk = w1 - w0 <= 32 * kEvictChunk;
+  const bool one_chunk = w1 - w0 <= 32 * kChunk;
   load(w0);
 
-  constexpr int kCopies = 4;  // histograms of a CTA, by lane: fewer lanes meet at a bin
-  __shared__ uint32_t hist[kCopies][kEvictBins];
-  __shared__ uint32_t sums[4][kEvictBins];   // the CTA's, one for each pass: read by the whole cluster
-  __shared__ uint32_t all[kEvictBins];       // the cluster's
-  __shared__ uint32_t found[2];              // bin, candidates above it
+  constexpr int kRounds = 3;
+  __shared__ uint4 hist4[kRounds][kEvictBins / 4];  // read by the whole cluster
+  __shared__ uint32_t warp_sums[kRounds][kEvictWarps];
+  __shared__ uint32_t found[kRounds][2];     // bin, candidates above it
   __shared__ uint32_t counts[2];             // this CTA's kept: above the threshold, equal to it
   __shared__ uint32_t warp_counts[2][kEvictWarps];
 
   uint32_t prefix = 0;
   uint32_t rest = static_cast<uint32_t>(wanted);  // still to take among those that share the prefix
   if (wanted > 0) {
+    static_assert(kEvictBins == 4 * kEvictThreads, "a thread has four bins");
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) hist4[i][tid] = make_uint4(0, 0, 0, 0);
+    if (parts > 1) cluster_barrier();  // the first CTA's bins are clear before others add to them
+    else __syncthreads();
 #pragma unroll 1
-    for (int pass = 0; pass < 4; ++pass) {
-      const int shift = 24 - 8 * pass;
-      for (int i = tid; i < kCopies * kEvictBins; i += kEvictThreads) hist[0][i] = 0;
-      __syncthreads();
-      for (int j = w0; j < w1; j += 32 * kEvictChunk) {
+    for (int round = 0; round < kRounds; ++round) {
+      const int shift = round == 0 ? 21 : (round == 1 ? 10 : 0), bits = round == 2 ? 10 : 11;
+      uint32_t* hist = reinterpret_cast<uint32_t*>(hist4[round]);
+      for (int j = w0; j < w1; j += 32 * kChunk) {
         if (!one_chunk) load(j);
 #pragma unroll
-        for (int i = 0; i < kEvictChunk; ++i) {
+        for (int i = 0; i < kChunk; ++i) {
           const uint32_t k = key[i];
-          if (k != 0 && (pass == 0 || ((k ^ prefix) >> (shift + 8)) == 0))
-            atomicAdd(&hist[lane % kCopies][(k >> shift) & 255u], 1u);
+          if (k != 0 && (round == 0 || ((k ^ prefix) >> (shift + bits)) == 0))
+            atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1u);
         }
       }
       __syncthreads();
-      if (tid < kEvictBins) {
-        uint32_t t = 0;
+      if (parts > 1) {
+        if (rank != 0) {
 #pragma unroll
-        for (int i = 0; i < kCopies; ++i) t += hist[i][tid];
-        sums[pass][tid] = t;
-      }
-      cluster_barrier();
-      if (tid < kEvictBins) {
-        uint32_t t[8];  // all requested before the first is used
-#pragma unroll
-        for (uint32_t r = 0; r < 8; ++r) t[r] = r < parts ? ld_cluster_u32(&sums[pass][tid], r) : 0u;
-        all[tid] = ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
-      }
-      __syncthreads();
-      if (warp == 0) {
-        // lane l holds bins 255 - 8 l .. 248 - 8 l, from the top
-        uint32_t t[8], mine = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          t[i] = all[255 - 8 * lane - i];
-          mine += t[i];
+          for (int i = 0; i < 4; ++i) {  // (lanes beside each other add to neighbouring bins)
+            const uint32_t c = hist[tid + i * kEvictThreads];
+            if (c != 0) add_cluster_u32(hist + tid + i * kEvictThreads, 0, c);
+          }
         }
+        cluster_barrier();
+      }
+      if (rank == 0) {
+        // bins from the top: thread t has 2047 - 4 t (t[0]) .. 2044 - 4 t (t[3])
+        const uint4 v = hist4[round][kEvictThreads - 1 - tid];
+        const uint32_t t[4] = {v.w, v.z, v.y, v.x};
+        const uint32_t mine = t[0] + t[1] + t[2] + t[3];
         uint32_t before = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const uint32_t v = __shfl_up_sync(0xffffffffu, before, o);
-          if (lane >= o) before += v;
+          const uint32_t y = __shfl_up_sync(0xffffffffu, before, o);
+          if (lane >= o) before += y;
         }
+        if (lane == 31) warp_sums[round][warp] = before;
+        __syncthreads();
         before -= mine;  // candidates in higher bins
+#pragma unroll
+        for (int i = 0; i < kEvictWarps; ++i) before += i < warp ? warp_sums[round][i] : 0u;
         if (before < rest && before + mine >= rest) {
           uint32_t above = before;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < 4; ++i) {
             if (above < rest && above + t[i] >= rest) {
-              found[0] = static_cast<uint32_t>(255 - 8 * lane - i);
-              found[1] = above;
+              const uint32_t bin = static_cast<uint32_t>(kEvictBins - 1 - 4 * tid - i);
+              for (uint32_t r = 0; r < parts; ++r) {
+                st_cluster_u32(&found[round][0], r, bin);
+                st_cluster_u32(&found[round][1], r, above);
+              }
             }
             above += t[i];
           }
         }
       }
-      __syncthreads();
-      prefix |= found[0] << shift;
-      rest -= found[1];
+      if (parts > 1) cluster_barrier();
+      else __syncthreads();
+      prefix |= found[round][0] << shift;
+      rest -= found[round][1];
     }
   }
   const uint32_t threshold = prefix;
   // kept candidates: key > threshold, and the first `rest` of those equal to it
   uint32_t above = 0, equal = 0;
   if (wanted > 0) {
-    for (int j = w0; j < w1; j += 32 * kEvictChunk) {
+    for (int j = w0; j < w1; j += 32 * kChunk) {
       if (!one_chunk) load(j);
 #pragma unroll
-      for (int i = 0; i < kEvictChunk; ++i) {
+      for (int i = 0; i < kChunk; ++i) {
         above += key[i] > threshold;
         equal += key[i] == threshold;
       }
@@ -202,7 +221,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const Evict
     for (int i = 0; i < kEvictWarps; ++i) t += warp_counts[tid][i];
     counts[tid] = t;
   }
-  cluster_barrier();
+  if (parts > 1) cluster_barrier();
   uint32_t place = 0, seen = 0;  // candidates above / equal before this warp's
 #pragma unroll
   for (uint32_t r = 0; r < 7; ++r) {
@@ -211,7 +230,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const Evict
       seen += ld_cluster_u32(&counts[1], r);
     }
   }
-  cluster_barrier();  // nobody leaves while its counts or histograms may be read
+  if (parts > 1) cluster_barrier();  // nobody leaves while its counts or histograms may be read
   for (int i = 0; i < warp; ++i) {
     place += warp_counts[0][i];
     seen += warp_counts[1][i];
@@ -220,10 +239,10 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const Evict
     // place: candidates kept before this one
     place += min(seen, rest);
     const uint32_t below = (1u << lane) - 1u;
-    for (int j = w0; j < w1; j += 32 * kEvictChunk) {
+    for (int j = w0; j < w1; j += 32 * kChunk) {
       if (!one_chunk) load(j);
 #pragma unroll
-      for (int i = 0; i < kEvictChunk; ++i) {
+      for (int i = 0; i < kChunk; ++i) {
         const bool eq = key[i] == threshold;
         const uint32_t eq_mask = __ballot_sync(0xffffffffu, eq);
         const bool take = key[i] > threshold || (eq && seen + __popc(eq_mask & below) < rest);

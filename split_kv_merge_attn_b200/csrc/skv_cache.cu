@@ -6,6 +6,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -164,8 +165,16 @@ int launch_decode_kv8(const CUtensorMap& tk, const CUtensorMap& tv, const Kv8Dec
                       skv_stream_t st) {
   using Cfg = Kv8DecodeCfg<D>;
   auto kern = decode_kv8_kernel<D, T, kE4M3, kLogits>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmemBytes);
+  static std::atomic<uint64_t> ready{0};  // devices (below 64) the limit is set on
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (bit == 0 || (ready.load(std::memory_order_relaxed) & bit) == 0) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
   return launch(kern, grid, kKv8Threads, Cfg::kSmemBytes, st, 1, tk, tv, a);
 }
 
@@ -557,14 +566,18 @@ skv_status kv8_evict(const void* k_codes, const void* v_codes, const float* k_sc
   a.budget = budget;
   a.sink = sink;
   a.recent = recent;
-  // 4096 tokens a CTA, or 8192 (all a warp's keys still in registers) where that
-  // many CTAs would not be resident at once; at most 8 CTAs a cluster
+  // as many tokens a CTA as keep a warp's keys in registers: 4096 (fewer only add
+  // rounds through the cluster: 8 heads of 4096 took 9.8 us, 12.1 with 2048 a CTA), or
+  // 8192 where CTAs of 4096 would not be resident at once; at most 8 CTAs a cluster
   const int sms = sm_count();
   if (sms <= 0) return cuda_status(cudaErrorNoDevice);
-  const int64_t each = static_cast<int64_t>(B) * Hkv * ceil_div64(capacity, 4096) > 2 * sms ? 8192 : 4096;
+  const int64_t bh = static_cast<int64_t>(B) * Hkv;
+  const int64_t each = bh * std::min<int64_t>(8, ceil_div64(capacity, 4096)) > 2 * sms ? 8192 : 4096;
   unsigned cluster = 1;
   while (cluster < 8 && cluster * each < capacity) cluster *= 2;
-  int e = launch(evict_select_kernel, dim3(cluster, static_cast<unsigned>(B * Hkv)), kEvictThreads, 0, stream, cluster, a);
+  const dim3 sgrid(cluster, static_cast<unsigned>(bh));
+  int e = ceil_div64(capacity, cluster) > 4096 ? launch(evict_select_kernel<16>, sgrid, kEvictThreads, 0, stream, cluster, a)
+                                               : launch(evict_select_kernel<8>, sgrid, kEvictThreads, 0, stream, cluster, a);
   if (e) return cuda_status(e);
   const int64_t most = std::min(budget, capacity);
   const dim3 grid(static_cast<unsigned>(ceil_div64(most, kKv8Window)), static_cast<unsigned>(B * Hkv));
