@@ -227,9 +227,9 @@ Kv8Ws kv8_ws_layout(int B, int Hq, int Hkv, int Lq, int capacity, int D, int cta
 
 template <typename T>
 int launch_kv8_merge(const Kv8DecodeArgs& a, int D, int ctas, unsigned rows, skv_stream_t st) {
-  if (D == 64) return launch(kv8_merge_kernel<64, T>, dim3(rows), 256, 0, st, 1, a, ctas);
-  if (D == 128) return launch(kv8_merge_kernel<128, T>, dim3(rows), 256, 0, st, 1, a, ctas);
-  return launch(kv8_merge_kernel<256, T>, dim3(rows), 256, 0, st, 1, a, ctas);
+  if (D == 64) return launch(kv8_merge_kernel<64, T>, dim3(rows, D / 64), 256, 0, st, 1, a, ctas);
+  if (D == 128) return launch(kv8_merge_kernel<128, T>, dim3(rows, D / 64), 256, 0, st, 1, a, ctas);
+  return launch(kv8_merge_kernel<256, T>, dim3(rows, D / 64), 256, 0, st, 1, a, ctas);
 }
 
 }  // namespace
