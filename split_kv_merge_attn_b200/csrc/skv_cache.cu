@@ -509,8 +509,9 @@ skv_status attn_splitkv_decode_kv8(const void* q, const void* k_codes, const voi
     wa.Hkv = Hkv;
     wa.rows = static_cast<int>(group_rows);
     wa.capacity = capacity;
-    const dim3 wgrid(static_cast<unsigned>(ceil_div64(capacity, 1024)), static_cast<unsigned>(B * Hkv));
-    e = launch(kv8_weights_kernel, wgrid, 256, 0, stream, 1, wa);
+    const dim3 wgrid(static_cast<unsigned>(ceil_div64(capacity, 4 * kWeightThreads)), static_cast<unsigned>(B * Hkv));
+    e = group_rows <= 2 ? launch(kv8_weights_kernel<2>, wgrid, kWeightThreads, 0, stream, 1, wa)
+                        : launch(kv8_weights_kernel<8>, wgrid, kWeightThreads, 0, stream, 1, wa);
   }
   return cuda_status(e);
 }
