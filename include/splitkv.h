@@ -1,13 +1,18 @@
 /*
  * splitkv.h -- C ABI of the B200 (sm_100a) attention-with-LSE library.
  *
- * Three device operations and their host-side planning helpers:
+ * The attention operations and their host-side planning helpers:
  *
  *   attn_fwd_lse         prefill / varlen attention forward writing O and one
  *                        log2 LSE per query row;
  *   attn_splitkv_decode  split-KV decode for 1..4 query rows per head with a
  *                        stable per-split online softmax, merged on device;
- *   merge_state          combines partial (O, LSE) pairs of disjoint KV ranges.
+ *   merge_state          combines partial (O, LSE) pairs of disjoint KV ranges;
+ *
+ * and, around an 8-bit key/value cache: rope_apply (rotary positions),
+ * kv8_append and kv8_fetch (in and out of the cache), attn_splitkv_decode_kv8
+ * (decode over it, with the keys' attention weights), kv8_evict (cuts it to a
+ * budget by those weights).
  *
  * The quantity (all entry points): for query row i of head h and the KV range J
  * of the call, s_j = scale * q_i . k_j and
@@ -422,7 +427,11 @@ skv_status rope_inv_freq(int rotary_dim, double base, skv_rope_scaling scaling, 
  * (tokens per scale) is 16, 32, 64 or 128 and divides capacity; D is 64, 128 or
  * 256.  Nothing needs initialising: what lies behind a sequence's last token is
  * never used, and stays as it is.  Codes must be finite (no e4m3 NaN) where
- * tokens are. */
+ * tokens are.
+ * Errors of the calls below: SKV_ERR_INVALID_ARG for NULL or misaligned pointers,
+ * bad sizes, and memory that is written and also read or written elsewhere by the
+ * call; SKV_ERR_UNSUPPORTED for fp32, other D or block, B * Hkv > 65535 or
+ * B * Hkv * capacity > 2^31 - 4096. */
 typedef enum { SKV_INT8 = 0, SKV_E4M3 = 1 } skv_code;
 
 /* kv8_append: quantises new tokens into the cache.

@@ -46,6 +46,22 @@ bool overlap(const void* p, size_t np, const void* q, size_t nq) {
   return p != nullptr && q != nullptr && a < b + nq && b < a + np;
 }
 
+struct Span {
+  const void* p;
+  size_t n;
+};
+// Whether anything written shares a byte with anything read or with another output.
+template <size_t kIn, size_t kOut>
+bool clash(const Span (&in)[kIn], const Span (&to)[kOut]) {
+  for (size_t i = 0; i < kOut; ++i) {
+    for (const Span& x : in)
+      if (overlap(to[i].p, to[i].n, x.p, x.n)) return true;
+    for (size_t j = 0; j < i; ++j)
+      if (overlap(to[i].p, to[i].n, to[j].p, to[j].n)) return true;
+  }
+  return false;
+}
+
 // Launches `kern` as a programmatic dependent of the kernel before it on the
 // stream (every kernel here waits for that one before it touches memory), in
 // clusters of `cluster` CTAs along x.
@@ -355,6 +371,12 @@ skv_status kv8_append(const void* k_new, const void* v_new, void* k_codes, void*
     return SKV_ERR_INVALID_ARG;
   if (skv_status s = check_cache(k_codes, v_codes, k_scale, v_scale, B, Hkv, capacity, D, block, codes)) return s;
   if (skv_status s = check_half(dtype)) return s;
+  const size_t heads = static_cast<size_t>(B) * Hkv, nb = static_cast<size_t>(B) * 4;
+  const size_t fresh = (layout == SKV_TND ? static_cast<size_t>(T) * Hkv : heads * S) * D * 2;
+  const Span in[] = {{k_new, fresh}, {v_new, fresh}, {start, nb}, {num_new, nb}, {cu_seqlens, nb + 4}};
+  const Span to[] = {{k_codes, heads * capacity * D}, {v_codes, heads * capacity * D},
+                     {k_scale, heads * (capacity / block) * 4}, {v_scale, heads * (capacity / block) * 4}};
+  if (clash(in, to)) return SKV_ERR_INVALID_ARG;
   if (S == 0) return SKV_OK;
   Kv8AppendArgs a;
   a.x[0] = k_new;
@@ -390,6 +412,12 @@ skv_status kv8_fetch(const void* k_codes, const void* v_codes, const float* k_sc
     return SKV_ERR_INVALID_ARG;
   if (skv_status s = check_cache(k_codes, v_codes, k_scale, v_scale, B, Hkv, capacity, D, block, codes)) return s;
   if (skv_status s = check_half(dtype)) return s;
+  const size_t heads = static_cast<size_t>(B) * Hkv, nb = static_cast<size_t>(B) * 4, window = heads * n * D * 2;
+  const Span in[] = {{k_codes, heads * capacity * D}, {v_codes, heads * capacity * D},
+                     {k_scale, heads * (capacity / block) * 4}, {v_scale, heads * (capacity / block) * 4},
+                     {start, nb}, {kv_len, nb}};
+  const Span to[] = {{k_out, window}, {v_out, window}};
+  if (clash(in, to)) return SKV_ERR_INVALID_ARG;
   if (n == 0) return SKV_OK;
   Kv8FetchArgs a;
   a.codes[0] = static_cast<const uint8_t*>(k_codes);
@@ -454,6 +482,13 @@ skv_status attn_splitkv_decode_kv8(const void* q, const void* k_codes, const voi
   const Kv8Ws w = kv8_ws_layout(B, Hq, Hkv, Lq, capacity, D, ctas, weights != nullptr);
   if (workspace_bytes < w.total) return SKV_ERR_WORKSPACE_TOO_SMALL;
   if (w.total > 0 && !good(workspace, 256)) return SKV_ERR_INVALID_ARG;
+  const size_t heads = static_cast<size_t>(B) * Hkv;
+  const Span in[] = {{q, static_cast<size_t>(rows) * D * 2}, {k_codes, heads * capacity * D},
+                     {v_codes, heads * capacity * D}, {k_scale, heads * (capacity / block) * 4},
+                     {v_scale, heads * (capacity / block) * 4}, {kv_len, static_cast<size_t>(B) * 4}};
+  const Span to[] = {{out, static_cast<size_t>(rows) * D * 2}, {lse, static_cast<size_t>(rows) * 4},
+                     {weights, heads * capacity * 4}, {workspace, w.total}};
+  if (clash(in, to)) return SKV_ERR_INVALID_ARG;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   float* merged = lse;  // the LSE the weights are taken against
   if (weights != nullptr && lse == nullptr) merged = reinterpret_cast<float*>(ws + w.lse);
@@ -530,21 +565,15 @@ skv_status kv8_evict(const void* k_codes, const void* v_codes, const float* k_sc
   if (skv_status s = check_cache(to_k_codes, to_v_codes, to_k_scale, to_v_scale, B, Hkv, to_capacity, D, block, codes))
     return s;
   if (budget > to_capacity) return SKV_ERR_INVALID_ARG;
-  // nothing written may overlap anything read or another output
   const size_t heads = static_cast<size_t>(B) * Hkv;
-  const struct { const void* p; size_t n; } in[] = {
-      {k_codes, heads * capacity * D}, {v_codes, heads * capacity * D}, {k_scale, heads * (capacity / block) * 4},
-      {v_scale, heads * (capacity / block) * 4}, {weights, heads * capacity * 4}, {kv_len, static_cast<size_t>(B) * 4}};
-  const struct { const void* p; size_t n; } to[] = {
-      {to_k_codes, heads * to_capacity * D}, {to_v_codes, heads * to_capacity * D},
-      {to_k_scale, heads * (to_capacity / block) * 4}, {to_v_scale, heads * (to_capacity / block) * 4},
-      {to_weights, heads * to_capacity * 4}, {kept, heads * budget * 4}, {new_len, static_cast<size_t>(B) * 4}};
-  for (size_t i = 0; i < sizeof(to) / sizeof(to[0]); ++i) {
-    for (const auto& x : in)
-      if (overlap(to[i].p, to[i].n, x.p, x.n)) return SKV_ERR_INVALID_ARG;
-    for (size_t j = 0; j < i; ++j)
-      if (overlap(to[i].p, to[i].n, to[j].p, to[j].n)) return SKV_ERR_INVALID_ARG;
-  }
+  const Span in[] = {{k_codes, heads * capacity * D}, {v_codes, heads * capacity * D},
+                     {k_scale, heads * (capacity / block) * 4}, {v_scale, heads * (capacity / block) * 4},
+                     {weights, heads * capacity * 4}, {kv_len, static_cast<size_t>(B) * 4}};
+  const Span to[] = {{to_k_codes, heads * to_capacity * D}, {to_v_codes, heads * to_capacity * D},
+                     {to_k_scale, heads * (to_capacity / block) * 4}, {to_v_scale, heads * (to_capacity / block) * 4},
+                     {to_weights, heads * to_capacity * 4}, {kept, heads * budget * 4},
+                     {new_len, static_cast<size_t>(B) * 4}};
+  if (clash(in, to)) return SKV_ERR_INVALID_ARG;
   EvictArgs a;
   a.weights = weights;
   a.kv_len = kv_len;

@@ -275,3 +275,21 @@ def test_kept_by_hand():
     assert O.kv8_kept(w, 10, 4, 0, 0).tolist() == [0, 3, 7, 9]
     assert O.kv8_kept(w, 10, 9, 0, 0).tolist() == [0, 1, 2, 3, 5, 6, 7, 8, 9]
     assert O.kv8_kept(w, 3, 3, 1, 1).tolist() == [0, 1, 2]
+
+
+# ---------------------------------------------------------------- memory written twice, or written and read
+
+@pytest.mark.parametrize("call,kw", [
+    (append, dict(v=addr(0))), (append, dict(v=addr(0) + 2 * 2 * 128 * 128 - 16)), (append, dict(vs=addr(2))),
+    (append, dict(kn=addr(0))), (append, dict(vn=addr(1) - 16)), (append, dict(start=addr(2))),
+    (append, dict(num=addr(3) + 2 * 2 * 4 * 4 - 4)), (append, dict(kn=addr(8), k=addr(8) + 2 * 2 * 4 * 128 * 2 - 16)),
+    (append, dict(layout=2, cu=addr(3) - 8, T=8)),
+    (fetch, dict(vo=addr(8))), (fetch, dict(ko=addr(0))), (fetch, dict(vo=addr(3) - 16)), (fetch, dict(kv_len=addr(8))),
+    (fetch, dict(start=addr(9) + 2 * 2 * 4 * 128 * 2 - 4)),
+    (decode, dict(out=addr(8))), (decode, dict(out=addr(1))), (decode, dict(lse=addr(9))), (decode, dict(kv_len=addr(9))),
+    (decode, dict(w=addr(2), ws=addr(20), wsb=1 << 20)), (decode, dict(w=addr(5), ws=addr(5), wsb=1 << 20)),
+    (decode, dict(ctas=2, cap=512, ws=addr(9), wsb=1 << 20)), (decode, dict(ctas=2, cap=512, ws=addr(0), wsb=1 << 20)),
+    (evict, dict(tv=addr(6))), (evict, dict(tk=addr(1))), (evict, dict(new=addr(5))), (evict, dict(tw=addr(4))),
+])
+def test_overlaps_are_refused(call, kw):
+    assert call(**kw) == INVALID
