@@ -22,6 +22,7 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <optional>
 #include <sstream>
 #include <stdexcept>
 #include <string>
@@ -133,14 +134,26 @@ bool truth(PyObject* o) {
   return x != 0;
 }
 
-// The caller's stream (its address as an integer) or the device's current one.
-skv_stream_t stream_of(PyObject* o, int dev) {
-  if (o == Py_None)
-    return reinterpret_cast<skv_stream_t>(c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream());
-  void* p = PyLong_AsVoidPtr(o);
-  if (p == nullptr && PyErr_Occurred()) throw PythonError();
-  return static_cast<skv_stream_t>(p);
-}
+// Makes the tensors' device current for a call, and the caller's stream (its
+// address as an integer; None: the device's current one): what the call allocates
+// then belongs to the stream it runs on.  Memory of another stream could still be in
+// use there, and would be handed out again there before this call has run.
+class On {
+ public:
+  On(int dev, PyObject* stream) : device_(static_cast<c10::DeviceIndex>(dev)) {
+    if (stream != Py_None) {
+      void* p = PyLong_AsVoidPtr(stream);
+      if (p == nullptr && PyErr_Occurred()) throw PythonError();
+      stream_.emplace(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(p), static_cast<c10::DeviceIndex>(dev)));
+    }
+    handle = reinterpret_cast<skv_stream_t>(c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream());
+  }
+  skv_stream_t handle;
+
+ private:
+  c10::cuda::CUDAGuard device_;
+  std::optional<c10::cuda::CUDAStreamGuard> stream_;
+};
 
 at::Tensor empty(at::IntArrayRef shape, at::ScalarType dt, int dev) {
   return at::empty(shape, at::TensorOptions().dtype(dt).device(at::kCUDA, static_cast<c10::DeviceIndex>(dev)));
@@ -264,6 +277,7 @@ PyObject* py_rope_apply(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor& f = tensor(a[3], "inv_freq");
     const int64_t nf[1] = {f.numel()};
     const auto* pf = static_cast<const double*>(address(f, "inv_freq", nf, at::kDouble, dev));
+    const On on(dev, a[10]);
     at::Tensor qo, ko;
     void* pqo = opt(a[8], "q_out", q.sizes(), dt, dev);
     void* pko = opt(a[9], "k_out", k_shape, dt, dev);
@@ -276,10 +290,9 @@ PyObject* py_rope_apply(PyObject*, PyObject* const* a, Py_ssize_t n) {
       pko = ko.data_ptr();
     }
     if (B * S > 0) {
-      const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
       check(g_lib.rope_apply(pq, pk, pqo, pko, pp, pf, small(B, "B"), small(Hq, "Hq"), small(Hkv, "Hkv"), small(S, "S"),
                              small(D, "D"), small(2 * nf[0], "inv_freq"), static_cast<float>(real(a[6])), code,
-                             static_cast<skv_layout>(layout), truth(a[5]), truth(a[7]), stream_of(a[10], dev)),
+                             static_cast<skv_layout>(layout), truth(a[5]), truth(a[7]), on.handle),
             "rope_apply");
     }
     return pair(result(a[8], qo), result(a[9], ko));
@@ -314,11 +327,11 @@ PyObject* py_kv8_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const auto* pn = static_cast<const int32_t*>(opt(a[4], "num_new", b, at::kInt, dev));
     const auto* pc = static_cast<const int32_t*>(opt(a[6], "cu_seqlens", b1, at::kInt, dev));
     const skv_dtype code = half(dt, "k");
+    const On on(dev, a[8]);
     if (S != 0 && (T != 0 || layout != SKV_TND)) {
-      const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
       check(g_lib.kv8_append(pk, pv, c.k, c.v, c.ks, c.vs, ps, pn, pc, static_cast<int>(c.B), static_cast<int>(c.Hkv),
                              small(S, "S"), small(T, "tokens"), static_cast<int>(c.capacity), static_cast<int>(c.D), c.block,
-                             code, c.code, static_cast<skv_layout>(layout), stream_of(a[8], dev)),
+                             code, c.code, static_cast<skv_layout>(layout), on.handle),
             "kv8_append");
     }
     return Py_NewRef(Py_None);
@@ -347,6 +360,7 @@ PyObject* py_kv8_fetch(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t b[1] = {c.B};
     const auto* ps = static_cast<const int32_t*>(opt(a[3], "start", b, at::kInt, dev));
     const auto* pl = static_cast<const int32_t*>(opt(a[4], "kv_len", b, at::kInt, dev));
+    const On on(dev, a[8]);
     at::Tensor ko, vo;
     void* pk = opt(a[6], "k_out", shape, dt, dev);
     void* pv = opt(a[7], "v_out", shape, dt, dev);
@@ -359,10 +373,9 @@ PyObject* py_kv8_fetch(PyObject*, PyObject* const* a, Py_ssize_t n) {
       pv = vo.data_ptr();
     }
     if (rows != 0) {
-      const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
       check(g_lib.kv8_fetch(c.k, c.v, c.ks, c.vs, pk, pv, ps, pl, static_cast<int>(c.B), static_cast<int>(c.Hkv), rows,
                             static_cast<int>(c.capacity), static_cast<int>(c.D), c.block, code, c.code,
-                            static_cast<skv_layout>(layout), stream_of(a[8], dev)),
+                            static_cast<skv_layout>(layout), on.handle),
             "kv8_fetch");
     }
     return pair(result(a[6], ko), result(a[7], vo));
@@ -390,6 +403,7 @@ PyObject* py_decode_kv8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     check(g_lib.plan(iB, iHq, iHkv, iLq, iN, iD, at::cuda::getDeviceProperties(static_cast<c10::DeviceIndex>(dev))->multiProcessorCount,
                      ctas, &ctas),
           "attn_splitkv_decode_kv8");
+    const On on(dev, a[11]);
     at::Tensor out, lse, ws;
     void* po = opt(a[7], "out", shape, dt, dev);
     if (a[7] == Py_None) {
@@ -418,9 +432,8 @@ PyObject* py_decode_kv8(PyObject*, PyObject* const* a, Py_ssize_t n) {
       }
     }
     const float scale = a[2] == Py_None ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(c.D))) : static_cast<float>(real(a[2]));
-    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
     check(g_lib.decode(pq, c.k, c.v, c.ks, c.vs, po, pl, pw, iB, iHq, iHkv, iLq, iN, iD, c.block, scale, code, c.code, pn,
-                       truth(a[4]), ctas, pws, bytes, stream_of(a[11], dev)),
+                       truth(a[4]), ctas, pws, bytes, on.handle),
           "attn_splitkv_decode_kv8");
     return pair(result(a[7], out), want_lse ? result(a[8], lse) : Py_NewRef(Py_None));
   });
@@ -442,6 +455,7 @@ PyObject* py_kv8_evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const auto* pw = static_cast<const float*>(arg(a[2], "weights", from, at::kFloat, dev));
     auto* pt = static_cast<float*>(arg(a[3], "to_weights", to, at::kFloat, dev));
     const auto* pn = static_cast<const int32_t*>(opt(a[4], "kv_len", b, at::kInt, dev));
+    const On on(dev, a[10]);
     at::Tensor kept, len;
     auto* pk = static_cast<int32_t*>(opt(a[8], "kept", bhk, at::kInt, dev));
     auto* pl = static_cast<int32_t*>(opt(a[9], "new_len", b, at::kInt, dev));
@@ -453,10 +467,9 @@ PyObject* py_kv8_evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
       len = empty(b, at::kInt, dev);
       pl = static_cast<int32_t*>(len.data_ptr());
     }
-    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
     check(g_lib.evict(c.k, c.v, c.ks, c.vs, pw, pn, t.k, t.v, t.ks, t.vs, pt, pk, pl, static_cast<int>(c.B),
                       static_cast<int>(c.Hkv), static_cast<int>(c.capacity), static_cast<int>(t.capacity),
-                      static_cast<int>(c.D), c.block, c.code, budget, sink, recent, stream_of(a[10], dev)),
+                      static_cast<int>(c.D), c.block, c.code, budget, sink, recent, on.handle),
           "kv8_evict");
     return pair(result(a[8], kept), result(a[9], len));
   });

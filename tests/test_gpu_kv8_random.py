@@ -190,3 +190,23 @@ def test_refusals_of_device_tensors():
         with pytest.raises(TypeError):
             bad()
     assert skv.launch_count() == before
+
+
+def test_memory_of_a_call_belongs_to_its_stream():
+    """A call given a stream allocates its workspace and outputs there: the current
+    stream, which goes on at once, must not get that memory before the call has run."""
+    B, Hq, Hkv, D, capacity = 1, 8, 2, 128, 16384
+    cache = filled_cache(B, Hkv, capacity, D, 64, "int8", [capacity], seed=1)
+    q = torch.randn(B, Hq, 1, D, generator=gen(1)).bfloat16().cuda()
+    w = torch.zeros(B, Hkv, capacity, device="cuda")
+    want = skv.attn_splitkv_decode_kv8(q, cache, weights=w)
+    again, s = torch.zeros_like(w), torch.cuda.Stream()
+    nbytes = skv.attn_splitkv_kv8_workspace(B, Hq, Hkv, 1, capacity, D, 296, True)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)  # the call waits about 10 ms behind this
+    out, lse = skv.attn_splitkv_decode_kv8(q, cache, weights=again, stream=s)
+    fills = [torch.full((nbytes,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    assert len(fills) == 4
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1]) and torch.equal(again, w)
