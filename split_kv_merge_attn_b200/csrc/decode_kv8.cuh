@@ -163,11 +163,13 @@ __device__ __forceinline__ void codes_to_half_even_odd(uint32_t w, uint32_t& h0,
 }
 
 // The weights of a tile from its scores s (x = s f): p = 2^(x - m), added to the
-// sums, and fp16 p vs / 2^mv, the A fragments of P V.
-template <int kGroups, bool kMasked>
+// sums, and fp16 p vs / 2^mv, the A fragments of P V.  kSplit: what that rounding
+// leaves, in fp16 too (pl).
+template <int kGroups, bool kMasked, bool kSplit>
 __device__ __forceinline__ void tile_weights(const float (&s)[2 * kGroups][4], const float (&f)[2][kGroups],
                                              const float (&lv)[kGroups], const float (&m)[2], const float (&mv)[2],
-                                             float (&lsum)[2], uint32_t (&pa)[kGroups][4]) {
+                                             float (&lsum)[2], uint32_t (&pa)[kGroups][4],
+                                             uint32_t (&pl)[kSplit ? kGroups : 1][4]) {
 #pragma unroll
   for (int hr = 0; hr < 2; ++hr) {
     uint64_t sum = f2_pack(0.f, 0.f);
@@ -195,6 +197,10 @@ __device__ __forceinline__ void tile_weights(const float (&s)[2 * kGroups][4], c
           pw.y = sb == -INFINITY ? 0.f : pw.y;
         }
         pa[gr][2 * i + hr] = pack_f16x2(pw.x, pw.y);
+        if constexpr (kSplit) {
+          const float2 kept = unpack2<__half>(pa[gr][2 * i + hr]);
+          pl[gr][2 * i + hr] = pack_f16x2(pw.x - kept.x, pw.y - kept.y);
+        }
       }
     }
     const float2 both = f2_unpack(sum);
@@ -478,9 +484,13 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
 #pragma unroll
   for (int j = 0; j < Cfg::kTilesN; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
 
+  // Weights of fp16 rounding (2^-11) vanish under a bf16 output's (2^-8); beside an
+  // fp16 output's they made the error 1.2 to 1.6 times that of rounding the output
+  // alone.  There a weight is two fp16 numbers (2^-22) and P V twice the MMAs.
+  constexpr bool kSplit = std::is_same<T, __half>::value;
   constexpr int kNt = kTileKeys / 8;
   // O += P V over one group of 16 keys, nvalid of them before the end
-  auto add_values = [&](uint32_t vt, int gr, const uint32_t (&pa)[4], int nvalid, auto partial) {
+  auto add_values = [&](uint32_t vt, int gr, const uint32_t (&pa)[4], const uint32_t (&pl)[4], int nvalid, auto partial) {
 #pragma unroll
     for (int c = 0; c < D / 16; c += 2) {
       // keys 0-7 and 8-15 of values 16 c .. 16 c + 15, then of the next 16
@@ -507,6 +517,10 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
         codes_to_half_even_odd<kE4M3>(v[2 * i + 1], e1, o1);
         mma_16816<__half>(o[2 * (c + i)], pa, e0, e1);
         mma_16816<__half>(o[2 * (c + i) + 1], pa, o0, o1);
+        if constexpr (kSplit) {
+          mma_16816<__half>(o[2 * (c + i)], pl, e0, e1);
+          mma_16816<__half>(o[2 * (c + i) + 1], pl, o0, o1);
+        }
       }
     }
   };
@@ -654,9 +668,9 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
         }
       }
     }
-    uint32_t pa[Cfg::kGroups][4];
-    if (masked) tile_weights<Cfg::kGroups, true>(s, f, lv, m, mv, lsum, pa);
-    else tile_weights<Cfg::kGroups, false>(s, f, lv, m, mv, lsum, pa);
+    uint32_t pa[Cfg::kGroups][4], pl[kSplit ? Cfg::kGroups : 1][4];
+    if (masked) tile_weights<Cfg::kGroups, true, kSplit>(s, f, lv, m, mv, lsum, pa, pl);
+    else tile_weights<Cfg::kGroups, false, kSplit>(s, f, lv, m, mv, lsum, pa, pl);
 
     // ---- O += P V
 #pragma unroll
@@ -667,12 +681,17 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
       const int key1 = key0 + ld * kKeys;
       if (key1 + kKeys <= s1) {
 #pragma unroll
-        for (int gr = 0; gr < kKeys / 16; ++gr) add_values(vt, gr, pa[ld * (kKeys / 16) + gr], 16, std::false_type{});
+        for (int gr = 0; gr < kKeys / 16; ++gr) {
+          const int at = ld * (kKeys / 16) + gr;
+          add_values(vt, gr, pa[at], pl[kSplit ? at : 0], 16, std::false_type{});
+        }
       } else {
 #pragma unroll
         for (int gr = 0; gr < kKeys / 16; ++gr)
-          if (key1 + 16 * gr < s1)
-            add_values(vt, gr, pa[ld * (kKeys / 16) + gr], s1 - key1 - 16 * gr, std::true_type{});
+          if (key1 + 16 * gr < s1) {
+            const int at = ld * (kKeys / 16) + gr;
+            add_values(vt, gr, pa[at], pl[kSplit ? at : 0], s1 - key1 - 16 * gr, std::true_type{});
+          }
       }
       __syncwarp();  // the whole warp has read this load
       if (lane == 0 && uv + Cfg::kStages < nloads) load(uv + Cfg::kStages, st_v, &tmV, 1, full_v);

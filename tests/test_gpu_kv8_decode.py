@@ -277,3 +277,28 @@ def test_inputs_written_just_before():
             out, lse = skv.attn_splitkv_decode_kv8(q, dst, kv_len=kl, weights=w)
     s.synchronize()
     check(q, src, out, lse, lengths, D ** -0.5, False, "bf16", O.to_f64(w))
+
+
+@pytest.mark.parametrize("codes", ["int8", "e4m3"])
+@pytest.mark.parametrize("G,Lq,D,n,causal,q_mult", [(1, 1, 64, 5000, False, 1.0), (4, 4, 128, 2000, True, 1.0),
+                                                    (1, 1, 128, 3001, False, 4.0), (8, 3, 64, 1000, False, 0.2),
+                                                    (4, 1, 256, 1500, False, 1.0)])
+def test_fp16_output_is_as_exact_as_its_rounding(codes, G, Lq, D, n, causal, q_mult):
+    """The rms error of an fp16 output is at most 1.1 times that of the oracle's O
+    rounded to fp16.  Rounding alone gives at least 2^-11 / sqrt(12) = 1.4e-4 of
+    |O|, so what the kernel may add to it is sqrt(1.1^2 - 1) * 1.4e-4 = 6.4e-5.  It
+    adds the weights' own error, 2^-22, and that of their exponents: fp32 sums of
+    D / 16 MMA steps are off by (D / 16) 2^-23 scale log2(e) sum |q k| ln 2 at
+    most, where |q| is 0.8 q_mult and |k| at most 1 (127 / 2 / 64) on average: 3e-6
+    at D = 64, 9e-6 at D = 128 (3.5e-5 with q_mult = 4), 2.4e-5 at D = 256.  Weights
+    rounded to fp16 once add 1.4e-4 or more."""
+    B, Hkv = 4, 8
+    capacity = -(-n // 64) * 64
+    cache = filled_cache(B, Hkv, capacity, D, 64, codes, [n] * B, seed=7, scale_span=0.0)
+    q = (q_mult * torch.randn(B, G * Hkv, Lq, D, generator=gen(8))).half().cuda()
+    out, _ = skv.attn_splitkv_decode_kv8(q, cache, kv_len=i32([n] * B), causal=causal)
+    k, v = values(cache.k, cache.k_scale, [n] * B), values(cache.v, cache.v_scale, [n] * B)
+    ref, _ = O.decode(q, k, v, D ** -0.5, kv_len=[n] * B, causal=causal)
+    rounded = torch.from_numpy(ref).half().double().numpy()
+    rms = lambda x: np.sqrt(np.mean(x * x))  # noqa: E731
+    assert rms(O.to_f64(out) - ref) <= 1.1 * rms(rounded - ref)
