@@ -164,14 +164,15 @@ __device__ __forceinline__ void codes_to_half_even_odd(uint32_t w, uint32_t& h0,
 
 // The weights of a tile from its scores s (x = s f): p = 2^(x - m), added to the
 // sums, and fp16 p vs / 2^mv, the A fragments of P V.  kSplit: what that rounding
-// leaves, in fp16 too (pl).
-template <int kGroups, bool kMasked, bool kSplit>
-__device__ __forceinline__ void tile_weights(const float (&s)[2 * kGroups][4], const float (&f)[2][kGroups],
-                                             const float (&lv)[kGroups], const float (&m)[2], const float (&mv)[2],
-                                             float (&lsum)[2], uint32_t (&pa)[kGroups][4],
+// leaves, in fp16 too (pl); kLow: the same in rows 8-15, which hold no rows of their
+// own (kHalves = 1).
+template <int kGroups, int kHalves, bool kMasked, bool kSplit, bool kLow>
+__device__ __forceinline__ void tile_weights(const float (&s)[2 * kGroups][4], const float (&f)[kHalves][kGroups],
+                                             const float (&lv)[kGroups], const float (&m)[kHalves],
+                                             const float (&mv)[kHalves], float (&lsum)[kHalves], uint32_t (&pa)[kGroups][4],
                                              uint32_t (&pl)[kSplit ? kGroups : 1][4]) {
 #pragma unroll
-  for (int hr = 0; hr < 2; ++hr) {
+  for (int hr = 0; hr < kHalves; ++hr) {
     uint64_t sum = f2_pack(0.f, 0.f);
     const uint64_t minus_m = f2_pack(-m[hr], -m[hr]);
 #pragma unroll
@@ -197,9 +198,11 @@ __device__ __forceinline__ void tile_weights(const float (&s)[2 * kGroups][4], c
           pw.y = sb == -INFINITY ? 0.f : pw.y;
         }
         pa[gr][2 * i + hr] = pack_f16x2(pw.x, pw.y);
-        if constexpr (kSplit) {
+        if constexpr (kSplit || kLow) {
           const float2 kept = unpack2<__half>(pa[gr][2 * i + hr]);
-          pl[gr][2 * i + hr] = pack_f16x2(pw.x - kept.x, pw.y - kept.y);
+          (kLow ? pa[gr][2 * i + 1] : pl[gr][2 * i + hr]) = pack_f16x2(pw.x - kept.x, pw.y - kept.y);
+        } else if constexpr (kHalves == 1) {
+          pa[gr][2 * i + 1] = 0u;
         }
       }
     }
@@ -208,7 +211,10 @@ __device__ __forceinline__ void tile_weights(const float (&s)[2 * kGroups][4], c
   }
 }
 
-template <int D, typename T, bool kE4M3, bool kLogits>
+// kHalves: 1 where a unit has at most 8 query rows (MMA rows 0-7), which leaves out
+// half the softmax, else 2 (with one row, bf16: B = 16, 16 heads, D = 64, 16384 keys, e4m3
+// 87.0 us against 95.5, int8 100.4 against 103.9; more rows need 2).
+template <int D, typename T, bool kE4M3, bool kLogits, int kHalves>
 __global__ void __launch_bounds__(kKv8Threads, 2)
     decode_kv8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const Kv8DecodeArgs a) {
@@ -326,479 +332,507 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
   uint32_t phase_k = 0, phase_v = 0;
   int seen = 0;                      // loads of the segments before
   while (w < w1) {
-  const int n = length(b);
-  const uint32_t unit_places = places(n);
-  if (w >= base + unit_places * heads) {  // the next sequence
-    base += unit_places * heads;
-    ++b;
-    continue;
-  }
-  const int uh = static_cast<int>((w - base) / unit_places);
-  const uint32_t p0 = w - base - uh * unit_places, p1 = min(unit_places, p0 + (w1 - w));
-  w += p1 - p0;
-  const int t_first = max(static_cast<int>(p0), 1) - 1, t_end = static_cast<int>(p1) - 1;
-  if (t_end <= t_first) continue;         // only the place without keys
-  const bool whole_unit = t_end - t_first == tiles(n);
-  const int hkv = uh / a.row_groups, rg = uh - hkv * a.row_groups;
-  const int s0 = t_first * kStride, s1 = min(n, t_end * kStride);
-  const int64_t bh = static_cast<int64_t>(b) * a.Hkv + hkv;
-  // this warp's tiles: keys first + t * kStride; loads u = kLoads * t + i of their
-  // kKeys keys, the last ones of which may lie behind the end
-  const int first = s0 + warp * kTileKeys;
-  const int ntiles = first < s1 ? (s1 - first + kStride - 1) / kStride : 0;
-  const int nloads = ntiles * Cfg::kLoads;
+    const int n = length(b);
+    const uint32_t unit_places = places(n);
+    if (w >= base + unit_places * heads) {  // the next sequence
+      base += unit_places * heads;
+      ++b;
+      continue;
+    }
+    const int uh = static_cast<int>((w - base) / unit_places);
+    const uint32_t p0 = w - base - uh * unit_places, p1 = min(unit_places, p0 + (w1 - w));
+    w += p1 - p0;
+    const int t_first = max(static_cast<int>(p0), 1) - 1, t_end = static_cast<int>(p1) - 1;
+    if (t_end <= t_first) continue;         // only the place without keys
+    const bool whole_unit = t_end - t_first == tiles(n);
+    const int hkv = uh / a.row_groups, rg = uh - hkv * a.row_groups;
+    const int s0 = t_first * kStride, s1 = min(n, t_end * kStride);
+    const int64_t bh = static_cast<int64_t>(b) * a.Hkv + hkv;
+    // this warp's tiles: keys first + t * kStride; loads u = kLoads * t + i of their
+    // kKeys keys, the last ones of which may lie behind the end
+    const int first = s0 + warp * kTileKeys;
+    const int ntiles = first < s1 ? (s1 - first + kStride - 1) / kStride : 0;
+    const int nloads = ntiles * Cfg::kLoads;
 
-  // load u of K (part 0) or V (1) into its stage (lane 0)
-  const int64_t token0 = bh * a.capacity + first;
-  auto load = [&](int u, int st, const CUtensorMap* map, int part, uint64_t* full) {
-    uint8_t* dst = ring + st * Cfg::kStageBytes + part * Cfg::kTileBytes;
-    const int64_t token = token0 + u / Cfg::kLoads * kStride + u % Cfg::kLoads * kKeys;
-    const int row = static_cast<int>(D == 64 ? token >> 1 : token);  // D = 64: two tokens in a 128-byte row
-    mbar_arrive_expect_tx(&full[st], Cfg::kTileBytes);
+    // load u of K (part 0) or V (1) into its stage (lane 0)
+    const int64_t token0 = bh * a.capacity + first;
+    auto load = [&](int u, int st, const CUtensorMap* map, int part, uint64_t* full) {
+      uint8_t* dst = ring + st * Cfg::kStageBytes + part * Cfg::kTileBytes;
+      const int64_t token = token0 + u / Cfg::kLoads * kStride + u % Cfg::kLoads * kKeys;
+      const int row = static_cast<int>(D == 64 ? token >> 1 : token);  // D = 64: two tokens in a 128-byte row
+      mbar_arrive_expect_tx(&full[st], Cfg::kTileBytes);
 #pragma unroll
-    for (int bx = 0; bx < Cfg::kBoxes; ++bx) tma_load_2d_once(dst + bx * kKeys * 128, map, &full[st], bx * 128, row, policy);
-  };
-  // ---- Q fragments: rows g and g + 8, this thread's share of every key row
-  // (32 contiguous values per box at 32 tq; 16 at 16 tq for D = 64)
-  constexpr int kShare = D == 64 ? 16 : 32;
-  uint32_t qa[D == 256 ? 1 : Cfg::kSteps][4];
-  float qscale[2];
-  {
-    uint32_t raw[2][D / 8];
+      for (int bx = 0; bx < Cfg::kBoxes; ++bx)
+        tma_load_2d_once(dst + bx * kKeys * 128, map, &full[st], bx * 128, row, policy);
+    };
+    // ---- Q fragments: rows g and g + 8, this thread's share of every key row
+    // (32 contiguous values per box at 32 tq; 16 at 16 tq for D = 64)
+    constexpr int kShare = D == 64 ? 16 : 32;
+    uint32_t qa[D == 256 ? 1 : Cfg::kSteps][4];
+    float qscale[kHalves];
+    {
+      uint32_t raw[kHalves][D / 8];
 #pragma unroll
-    for (int hr = 0; hr < 2; ++hr) {
-      const int r = rg * kKv8Rows + g + 8 * hr;
+      for (int hr = 0; hr < kHalves; ++hr) {
+        const int r = rg * kKv8Rows + g + 8 * hr;
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) raw[hr][i] = 0;
-      if (r < rows_total) {
-        const int h = hkv * G + r / a.Lq;
-        const T* src = static_cast<const T*>(a.q) + ((static_cast<int64_t>(b) * a.Hq + h) * a.Lq + r % a.Lq) * D;
+        for (int i = 0; i < D / 8; ++i) raw[hr][i] = 0;
+        if (r < rows_total) {
+          const int h = hkv * G + r / a.Lq;
+          const T* src = static_cast<const T*>(a.q) + ((static_cast<int64_t>(b) * a.Hq + h) * a.Lq + r % a.Lq) * D;
 #pragma unroll
-        for (int bx = 0; bx < Cfg::kBoxes; ++bx)
+          for (int bx = 0; bx < Cfg::kBoxes; ++bx)
 #pragma unroll
-          for (int i = 0; i < kShare / 8; ++i) {
-            const uint4 u = __ldg(reinterpret_cast<const uint4*>(src + bx * 128 + tq * kShare) + i);
-            uint32_t* dst = &raw[hr][bx * 16 + i * 4];
-            dst[0] = u.x; dst[1] = u.y; dst[2] = u.z; dst[3] = u.w;
-          }
-      }
-    }
-    // the first tiles, behind q's loads: behind every CTA's tiles q arrived 3 to 4 us late
-    if (lane == 0) {
-      int st = st_k;  // = st_v between segments
-      for (int u = 0; u < min(nloads, Cfg::kStages); ++u) {
-        load(u, st, &tmK, 0, full_k);
-        load(u, st, &tmV, 1, full_v);
-        if (++st == Cfg::kStages) st = 0;
-      }
-    }
-    __syncwarp();
-#pragma unroll
-    for (int hr = 0; hr < 2; ++hr) {
-      uint32_t top = 0;
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) top = __vmaxu2(top, raw[hr][i] & 0x7fff7fffu);
-      top = max(top & 0xffffu, top >> 16);
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // 2^-e and 2^e of the row's largest magnitude in [2^e, 2^(e + 1)); 1 for a
-      // row of zeros (clamped where one of the powers would not be a normal number)
-      const float amax = unpack2<T>(top).x;
-      int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
-      e = amax > 0.f ? min(max(e, -126), 126) : 0;
-      const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-      qscale[hr] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        const float2 f = unpack2<T>(raw[hr][i]);
-        raw[hr][i] = pack_f16x2(f.x * down, f.y * down);
-      }
-    }
-    // step kk takes this thread's values 4 kk .. 4 kk + 3: two packed pairs
-    if constexpr (D == 256) {
-      if (warp == 0) {
-#pragma unroll
-        for (int kk = 0; kk < Cfg::kSteps; ++kk)
-          qfrag[kk * 32 + lane] = make_uint4(raw[0][2 * kk], raw[1][2 * kk], raw[0][2 * kk + 1], raw[1][2 * kk + 1]);
-      }
-      __syncthreads();
-    } else {
-#pragma unroll
-      for (int kk = 0; kk < Cfg::kSteps; ++kk) {
-        qa[kk][0] = raw[0][2 * kk];
-        qa[kk][1] = raw[1][2 * kk];
-        qa[kk][2] = raw[0][2 * kk + 1];
-        qa[kk][3] = raw[1][2 * kk + 1];
-      }
-    }
-  }
-  const float xs0 = a.scale_log2 * qscale[0], xs1 = a.scale_log2 * qscale[1];
-
-  // keys each of this thread's two rows may see; every row sees those below safe_end
-  int row_end[2] = {s1, s1};
-  int safe_end = s1;
-  if (a.causal) {
-    safe_end = min(s1, n - a.Lq + 1);
-#pragma unroll
-    for (int hr = 0; hr < 2; ++hr) {
-      const int i = (rg * kKv8Rows + g + 8 * hr) % a.Lq;
-      row_end[hr] = min(s1, max(n - a.Lq + 1 + i, 0));
-    }
-  }
-  float* lrow[2] = {nullptr, nullptr};  // this thread's logit rows
-  if constexpr (kLogits) {
-#pragma unroll
-    for (int hr = 0; hr < 2; ++hr) {
-      const int r = rg * kKv8Rows + g + 8 * hr;
-      if (r < rows_total) lrow[hr] = a.logits + (bh * rows_total + r) * a.capacity;
-    }
-  }
-
-  const float* ksc = a.k_scale + bh * (a.capacity >> a.block_shift);
-  const float* vsc = a.v_scale + bh * (a.capacity >> a.block_shift);
-  // 16 keys lie in one block of every block size, so a tile has one pair of scales
-  // for each group of 16.  A lane holds those of one group of the next 32 / kGroups
-  // tiles (0 for a group behind the last key), loaded that many tiles ahead: under
-  // load a scale takes longer to arrive than a tile to compute (one tile ahead cost
-  // 1.2 us of 31 at D = 128, 15 us of 110 at D = 64).
-  constexpr int kChunk = 32 / Cfg::kGroups;  // tiles of a chunk
-  float ks_chunk = 0.f, lv_chunk = 0.f, ks_ahead = 0.f, vs_ahead = 0.f;
-  auto fetch_scales = [&](int key0) {
-    const int64_t key = key0 + static_cast<int64_t>(lane / Cfg::kGroups) * kStride + lane % Cfg::kGroups * 16;
-    ks_ahead = key < s1 ? __ldg(ksc + (key >> a.block_shift)) : 0.f;
-    vs_ahead = key < s1 ? __ldg(vsc + (key >> a.block_shift)) : 0.f;
-  };
-  fetch_scales(first);
-  int chunk_tile = 0;  // the current tile's place in its chunk
-
-  // m and mv are references a little behind the running maxima of x and of
-  // x + log2 vs: they move only when a value lies more than 2^kSlack above, so
-  // most tiles need no reduction over a row and no rescaling.  p and the fp16
-  // weights p vs / 2^mv then reach 2^kSlack, far from fp16's limit.
-  constexpr float kSlack = 8.f;
-  constexpr float kNone = -1.0e30f;  // nothing seen yet
-  float m[2] = {kNone, kNone};
-  float mv[2] = {kNone, kNone};
-  float lsum[2] = {0.f, 0.f};
-  float o[Cfg::kTilesN][4];
-#pragma unroll
-  for (int j = 0; j < Cfg::kTilesN; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-
-  // Weights of fp16 rounding (2^-11) vanish under a bf16 output's (2^-8); beside an
-  // fp16 output's they made the error 1.2 to 1.6 times that of rounding the output
-  // alone.  There a weight is two fp16 numbers (2^-22) and P V twice the MMAs.
-  constexpr bool kSplit = std::is_same<T, __half>::value;
-  constexpr int kNt = kTileKeys / 8;
-  // O += P V over one group of 16 keys, nvalid of them before the end
-  auto add_values = [&](uint32_t vt, int gr, const uint32_t (&pa)[4], const uint32_t (&pl)[4], int nvalid, auto partial) {
-#pragma unroll
-    for (int c = 0; c < D / 16; c += 2) {
-      // keys 0-7 and 8-15 of values 16 c .. 16 c + 15, then of the next 16
-      const uint32_t key = gr * 16 + (lane & 15);
-      const int cc = c + (lane >> 4);
-      uint32_t addr;
-      if constexpr (D == 64) addr = vt + sw128(key >> 1, (key & 1) * 4 + cc);
-      else addr = vt + (c / 8) * kKeys * 128 + sw128(key, cc % 8);
-      uint32_t v[4];
-      ldmatrix_x4_trans(addr, v[0], v[1], v[2], v[3]);
-      if constexpr (decltype(partial)::value) {
-        // codes behind the last key may be anything (unfilled cache, e4m3 NaN):
-        // their weight is 0 and so must the codes be
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int k0 = 2 * tq + 8 * (i & 1);  // this register's keys: k0 (low half), k0 + 1
-          v[i] &= (k0 < nvalid ? 0xffffu : 0u) | (k0 + 1 < nvalid ? 0xffff0000u : 0u);
+            for (int i = 0; i < kShare / 8; ++i) {
+              const uint4 u = __ldg(reinterpret_cast<const uint4*>(src + bx * 128 + tq * kShare) + i);
+              uint32_t* dst = &raw[hr][bx * 16 + i * 4];
+              dst[0] = u.x; dst[1] = u.y; dst[2] = u.z; dst[3] = u.w;
+            }
         }
       }
+      // the first tiles, behind q's loads: behind every CTA's tiles q arrived 3 to 4 us late
+      if (lane == 0) {
+        int st = st_k;  // = st_v between segments
+        for (int u = 0; u < min(nloads, Cfg::kStages); ++u) {
+          load(u, st, &tmK, 0, full_k);
+          load(u, st, &tmV, 1, full_v);
+          if (++st == Cfg::kStages) st = 0;
+        }
+      }
+      __syncwarp();
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint32_t e0, o0, e1, o1;
-        codes_to_half_even_odd<kE4M3>(v[2 * i], e0, o0);
-        codes_to_half_even_odd<kE4M3>(v[2 * i + 1], e1, o1);
-        mma_16816<__half>(o[2 * (c + i)], pa, e0, e1);
-        mma_16816<__half>(o[2 * (c + i) + 1], pa, o0, o1);
-        if constexpr (kSplit) {
-          mma_16816<__half>(o[2 * (c + i)], pl, e0, e1);
-          mma_16816<__half>(o[2 * (c + i) + 1], pl, o0, o1);
+      for (int hr = 0; hr < kHalves; ++hr) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) top = __vmaxu2(top, raw[hr][i] & 0x7fff7fffu);
+        top = max(top & 0xffffu, top >> 16);
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // 2^-e and 2^e of the row's largest magnitude in [2^e, 2^(e + 1)); 1 for a
+        // row of zeros (clamped where one of the powers would not be a normal number)
+        const float amax = unpack2<T>(top).x;
+        int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
+        e = amax > 0.f ? min(max(e, -126), 126) : 0;
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        qscale[hr] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          const float2 f = unpack2<T>(raw[hr][i]);
+          raw[hr][i] = pack_f16x2(f.x * down, f.y * down);
+        }
+      }
+      // step kk takes this thread's values 4 kk .. 4 kk + 3: two packed pairs
+      if constexpr (D == 256) {
+        if (warp == 0) {
+#pragma unroll
+          for (int kk = 0; kk < Cfg::kSteps; ++kk)
+            qfrag[kk * 32 + lane] = make_uint4(raw[0][2 * kk], kHalves == 2 ? raw[kHalves - 1][2 * kk] : 0u,
+                                               raw[0][2 * kk + 1], kHalves == 2 ? raw[kHalves - 1][2 * kk + 1] : 0u);
+        }
+        __syncthreads();
+      } else {
+#pragma unroll
+        for (int kk = 0; kk < Cfg::kSteps; ++kk) {
+          qa[kk][0] = raw[0][2 * kk];
+          qa[kk][1] = kHalves == 2 ? raw[kHalves - 1][2 * kk] : 0u;
+          qa[kk][2] = raw[0][2 * kk + 1];
+          qa[kk][3] = kHalves == 2 ? raw[kHalves - 1][2 * kk + 1] : 0u;
         }
       }
     }
-  };
+    float xs[kHalves];
+#pragma unroll
+    for (int hr = 0; hr < kHalves; ++hr) xs[hr] = a.scale_log2 * qscale[hr];
 
-  // the warp gives up as one: a lane whose limit expires takes the others along
-  auto wait = [&](uint64_t* full, uint32_t phase) {
-    return __all_sync(0xffffffffu, mbar_wait(full, phase, abort_flag, kErrKv8FullWait)) != 0;
-  };
-  int uk = 0, uv = 0;  // loads of K and of V read so far
-  bool ok = true;
-  for (int key0 = first; key0 < s1; key0 += kStride) {
-    if (chunk_tile == 0) {
-      ks_chunk = ks_ahead;
-      lv_chunk = __log2f(vs_ahead);  // -inf for a block of zeros
-      fetch_scales(key0 + kChunk * kStride);
-    }
-    float f[2][Cfg::kGroups], lv[Cfg::kGroups];
+    // keys each of this thread's two rows may see; every row sees those below safe_end
+    int row_end[kHalves];
 #pragma unroll
-    for (int gr = 0; gr < Cfg::kGroups; ++gr) {
-      const float ks = __shfl_sync(0xffffffffu, ks_chunk, chunk_tile * Cfg::kGroups + gr);
-      lv[gr] = __shfl_sync(0xffffffffu, lv_chunk, chunk_tile * Cfg::kGroups + gr);
-      f[0][gr] = xs0 * ks;
-      f[1][gr] = xs1 * ks;
+    for (int hr = 0; hr < kHalves; ++hr) row_end[hr] = s1;
+    int safe_end = s1;
+    if (a.causal) {
+      safe_end = min(s1, n - a.Lq + 1);
+#pragma unroll
+      for (int hr = 0; hr < kHalves; ++hr) {
+        const int i = (rg * kKv8Rows + g + 8 * hr) % a.Lq;
+        row_end[hr] = min(s1, max(n - a.Lq + 1 + i, 0));
+      }
     }
-    chunk_tile = (chunk_tile + 1) % kChunk;
+    float* lrow[kHalves] = {};  // this thread's logit rows
+    if constexpr (kLogits) {
+#pragma unroll
+      for (int hr = 0; hr < kHalves; ++hr) {
+        const int r = rg * kKv8Rows + g + 8 * hr;
+        if (r < rows_total) lrow[hr] = a.logits + (bh * rows_total + r) * a.capacity;
+      }
+    }
 
-    // ---- S = Q K^T for 16 rows x kTileKeys keys
-    float s[kNt][4];
+    const float* ksc = a.k_scale + bh * (a.capacity >> a.block_shift);
+    const float* vsc = a.v_scale + bh * (a.capacity >> a.block_shift);
+    // 16 keys lie in one block of every block size, so a tile has one pair of scales
+    // for each group of 16.  A lane holds those of one group of the next 32 / kGroups
+    // tiles (0 for a group behind the last key), loaded that many tiles ahead: under
+    // load a scale takes longer to arrive than a tile to compute (one tile ahead cost
+    // 1.2 us of 31 at D = 128, 15 us of 110 at D = 64).
+    constexpr int kChunk = 32 / Cfg::kGroups;  // tiles of a chunk
+    float ks_chunk = 0.f, lv_chunk = 0.f, ks_ahead = 0.f, vs_ahead = 0.f;
+    auto fetch_scales = [&](int key0) {
+      const int64_t key = key0 + static_cast<int64_t>(lane / Cfg::kGroups) * kStride + lane % Cfg::kGroups * 16;
+      ks_ahead = key < s1 ? __ldg(ksc + (key >> a.block_shift)) : 0.f;
+      vs_ahead = key < s1 ? __ldg(vsc + (key >> a.block_shift)) : 0.f;
+    };
+    fetch_scales(first);
+    int chunk_tile = 0;  // the current tile's place in its chunk
+
+    // m and mv are references a little behind the running maxima of x and of
+    // x + log2 vs: they move only when a value lies more than 2^kSlack above, so
+    // most tiles need no reduction over a row and no rescaling.  p and the fp16
+    // weights p vs / 2^mv then reach 2^kSlack, far from fp16's limit.
+    constexpr float kSlack = 8.f;
+    constexpr float kNone = -1.0e30f;  // nothing seen yet
+    float m[kHalves], mv[kHalves], lsum[kHalves];
 #pragma unroll
-    for (int ld = 0; ld < Cfg::kLoads; ++ld) {
-      ok = ok && wait(&full_k[st_k], phase_k);
-      if (!ok) continue;
-      const uint8_t* kt = ring + st_k * Cfg::kStageBytes;
-      constexpr int kN = kKeys / 8;              // n-tiles of a load
-      constexpr int kChains = kN == 2 ? 2 : 1;   // with two n-tiles only, two chains of MMAs each
-      float sc[kN][kChains][4];
+    for (int hr = 0; hr < kHalves; ++hr) {
+      m[hr] = mv[hr] = kNone;
+      lsum[hr] = 0.f;
+    }
+    float o[Cfg::kTilesN][4];
 #pragma unroll
-      for (int nt = 0; nt < kN; ++nt)
+    for (int j = 0; j < Cfg::kTilesN; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+
+    // Weights of fp16 rounding (2^-11) vanish under a bf16 output's (2^-8); beside an
+    // fp16 output's they made the error 1.2 to 1.6 times that of rounding the output
+    // alone.  There a weight is two fp16 numbers (2^-22): of at most 8 rows, the second
+    // in rows 8-15, at no MMA (the whole call, B = 16, 16 heads, D = 64, 16384 keys, e4m3:
+    // 87.7 us against 107 with MMAs of its own and 87.0 for bf16); of 16, with twice
+    // the MMAs of P V (B = 2, 32 / 8 heads, Lq = 4, D = 128, 32768 keys, int8: 37.4 us
+    // against 31.4 for bf16).
+    constexpr bool kLow = std::is_same<T, __half>::value && kHalves == 1;
+    constexpr bool kSplit = std::is_same<T, __half>::value && kHalves == 2;
+    constexpr int kNt = kTileKeys / 8;
+    // O += P V over one group of 16 keys, nvalid of them before the end
+    auto add_values = [&](uint32_t vt, int gr, const uint32_t (&pa)[4], const uint32_t (&pl)[4], int nvalid,
+                          auto partial) {
 #pragma unroll
-        for (int i = 0; i < kChains; ++i) sc[nt][i][0] = sc[nt][i][1] = sc[nt][i][2] = sc[nt][i][3] = 0.f;
-#pragma unroll
-      for (int bx = 0; bx < Cfg::kBoxes; ++bx) {
-#pragma unroll
-        for (int half = 0; half < (D == 64 ? 1 : 2); ++half) {
-          uint4 kw[kN];
-#pragma unroll
-          for (int nt = 0; nt < kN; ++nt) {
-            const uint32_t key = nt * 8 + g;
-            uint32_t off;
-            if constexpr (D == 64) off = sw128(key >> 1, (key & 1) * 4 + tq);
-            else off = bx * kKeys * 128 + sw128(key, 2 * tq + half);
-            kw[nt] = *reinterpret_cast<const uint4*>(kt + off);
-          }
+      for (int c = 0; c < D / 16; c += 2) {
+        // keys 0-7 and 8-15 of values 16 c .. 16 c + 15, then of the next 16
+        const uint32_t key = gr * 16 + (lane & 15);
+        const int cc = c + (lane >> 4);
+        uint32_t addr;
+        if constexpr (D == 64) addr = vt + sw128(key >> 1, (key & 1) * 4 + cc);
+        else addr = vt + (c / 8) * kKeys * 128 + sw128(key, cc % 8);
+        uint32_t v[4];
+        ldmatrix_x4_trans(addr, v[0], v[1], v[2], v[3]);
+        if constexpr (decltype(partial)::value) {
+          // codes behind the last key may be anything (unfilled cache, e4m3 NaN):
+          // their weight is 0 and so must the codes be
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int kk = bx * 8 + half * 4 + i;
-            uint32_t aq[4];
-            if constexpr (D == 256) {
-              const uint4 u = qfrag[kk * 32 + lane];
-              aq[0] = u.x; aq[1] = u.y; aq[2] = u.z; aq[3] = u.w;
-            } else {
-              aq[0] = qa[kk][0]; aq[1] = qa[kk][1]; aq[2] = qa[kk][2]; aq[3] = qa[kk][3];
-            }
+            const int k0 = 2 * tq + 8 * (i & 1);  // this register's keys: k0 (low half), k0 + 1
+            v[i] &= (k0 < nvalid ? 0xffffu : 0u) | (k0 + 1 < nvalid ? 0xffff0000u : 0u);
+          }
+        }
 #pragma unroll
-            for (int nt = 0; nt < kN; ++nt) {
-              const uint32_t w = i == 0 ? kw[nt].x : (i == 1 ? kw[nt].y : (i == 2 ? kw[nt].z : kw[nt].w));
-              uint32_t b0, b1;
-              codes_to_half<kE4M3>(w, b0, b1);
-              mma_16816<__half>(sc[nt][i % kChains], aq, b0, b1);
-            }
+        for (int i = 0; i < 2; ++i) {
+          uint32_t e0, o0, e1, o1;
+          codes_to_half_even_odd<kE4M3>(v[2 * i], e0, o0);
+          codes_to_half_even_odd<kE4M3>(v[2 * i + 1], e1, o1);
+          mma_16816<__half>(o[2 * (c + i)], pa, e0, e1);
+          mma_16816<__half>(o[2 * (c + i) + 1], pa, o0, o1);
+          if constexpr (kSplit) {
+            mma_16816<__half>(o[2 * (c + i)], pl, e0, e1);
+            mma_16816<__half>(o[2 * (c + i) + 1], pl, o0, o1);
           }
         }
       }
-      __syncwarp();  // the whole warp has read this load
-      if (lane == 0 && uk + Cfg::kStages < nloads) load(uk + Cfg::kStages, st_k, &tmK, 0, full_k);
-      ++uk;
-      if (++st_k == Cfg::kStages) {
-        st_k = 0;
-        phase_k ^= 1u;
-      }
-#pragma unroll
-      for (int nt = 0; nt < kN; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          s[ld * kN + nt][e] = sc[nt][0][e];
-          if constexpr (kChains == 2) s[ld * kN + nt][e] += sc[nt][1][e];
-        }
-    }
-    if (!ok) break;
+    };
 
-    // ---- softmax (exp2 domain), rows g and g + 8
-    const bool masked = key0 + kTileKeys > safe_end;  // the same for the whole warp
-    if (masked) {
-#pragma unroll
-      for (int nt = 0; nt < kNt; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (key0 + nt * 8 + 2 * tq + (e & 1) >= row_end[e >> 1]) s[nt][e] = -INFINITY;
-    }
-    if constexpr (kLogits) {
-      // up to 16-key alignment the slots behind the last key are this warp's too
-      // (nothing reads them); the capacity is a multiple of 16
-#pragma unroll
-      for (int hr = 0; hr < 2; ++hr) {
-        if (lrow[hr] != nullptr) {
-#pragma unroll
-          for (int nt = 0; nt < kNt; ++nt)
-            if (key0 + nt / 2 * 16 < s1) {
-              const float sa = s[nt][2 * hr], sb = s[nt][2 * hr + 1], fx = f[hr][nt / 2];
-              *reinterpret_cast<float2*>(lrow[hr] + key0 + nt * 8 + 2 * tq) =
-                  make_float2(masked && sa == -INFINITY ? sa : sa * fx, masked && sb == -INFINITY ? sb : sb * fx);
-            }
-        }
+    // the warp gives up as one: a lane whose limit expires takes the others along
+    auto wait = [&](uint64_t* full, uint32_t phase) {
+      return __all_sync(0xffffffffu, mbar_wait(full, phase, abort_flag, kErrKv8FullWait)) != 0;
+    };
+    int uk = 0, uv = 0;  // loads of K and of V read so far
+    bool ok = true;
+    for (int key0 = first; key0 < s1; key0 += kStride) {
+      if (chunk_tile == 0) {
+        ks_chunk = ks_ahead;
+        lv_chunk = __log2f(vs_ahead);  // -inf for a block of zeros
+        fetch_scales(key0 + kChunk * kStride);
       }
-    }
-    float mx[2], vx[2];  // this lane's largest x, largest x + log2 vs
-#pragma unroll
-    for (int hr = 0; hr < 2; ++hr) {
+      float f[kHalves][Cfg::kGroups], lv[Cfg::kGroups];
 #pragma unroll
       for (int gr = 0; gr < Cfg::kGroups; ++gr) {
-        const float top = fmaxf(fmax3(s[2 * gr][2 * hr], s[2 * gr][2 * hr + 1], s[2 * gr + 1][2 * hr]),
-                                s[2 * gr + 1][2 * hr + 1]) * f[hr][gr];
-        mx[hr] = gr == 0 ? top : fmaxf(mx[hr], top);
-        vx[hr] = gr == 0 ? top + lv[gr] : fmaxf(vx[hr], top + lv[gr]);
+        const float ks = __shfl_sync(0xffffffffu, ks_chunk, chunk_tile * Cfg::kGroups + gr);
+        lv[gr] = __shfl_sync(0xffffffffu, lv_chunk, chunk_tile * Cfg::kGroups + gr);
+#pragma unroll
+        for (int hr = 0; hr < kHalves; ++hr) f[hr][gr] = xs[hr] * ks;
       }
-    }
-    const bool above = mx[0] > m[0] + kSlack || mx[1] > m[1] + kSlack || vx[0] > mv[0] + kSlack || vx[1] > mv[1] + kSlack;
-    if (__any_sync(0xffffffffu, above)) {
-#pragma unroll
-      for (int hr = 0; hr < 2; ++hr) {
-#pragma unroll
-        for (int sh = 1; sh < 4; sh <<= 1) {
-          mx[hr] = fmaxf(mx[hr], __shfl_xor_sync(0xffffffffu, mx[hr], sh));
-          vx[hr] = fmaxf(vx[hr], __shfl_xor_sync(0xffffffffu, vx[hr], sh));
-        }
-        const float mn = fmaxf(m[hr], mx[hr]), vn = fmaxf(mv[hr], vx[hr]);
-        lsum[hr] *= ex2_approx(m[hr] - mn);
-        const float al = ex2_approx(mv[hr] - vn);
-        m[hr] = mn;
-        mv[hr] = vn;
-#pragma unroll
-        for (int j = 0; j < Cfg::kTilesN; ++j) {
-          o[j][2 * hr] *= al;
-          o[j][2 * hr + 1] *= al;
-        }
-      }
-    }
-    uint32_t pa[Cfg::kGroups][4], pl[kSplit ? Cfg::kGroups : 1][4];
-    if (masked) tile_weights<Cfg::kGroups, true, kSplit>(s, f, lv, m, mv, lsum, pa, pl);
-    else tile_weights<Cfg::kGroups, false, kSplit>(s, f, lv, m, mv, lsum, pa, pl);
+      chunk_tile = (chunk_tile + 1) % kChunk;
 
-    // ---- O += P V
+      // ---- S = Q K^T for 16 rows x kTileKeys keys
+      float s[kNt][4];
 #pragma unroll
-    for (int ld = 0; ld < Cfg::kLoads; ++ld) {
-      ok = ok && wait(&full_v[st_v], phase_v);
-      if (!ok) continue;
-      const uint32_t vt = smem_u32(ring + st_v * Cfg::kStageBytes + Cfg::kTileBytes);
-      const int key1 = key0 + ld * kKeys;
-      if (key1 + kKeys <= s1) {
+      for (int ld = 0; ld < Cfg::kLoads; ++ld) {
+        ok = ok && wait(&full_k[st_k], phase_k);
+        if (!ok) continue;
+        const uint8_t* kt = ring + st_k * Cfg::kStageBytes;
+        constexpr int kN = kKeys / 8;              // n-tiles of a load
+        constexpr int kChains = kN == 2 ? 2 : 1;   // with two n-tiles only, two chains of MMAs each
+        float sc[kN][kChains][4];
 #pragma unroll
-        for (int gr = 0; gr < kKeys / 16; ++gr) {
-          const int at = ld * (kKeys / 16) + gr;
-          add_values(vt, gr, pa[at], pl[kSplit ? at : 0], 16, std::false_type{});
+        for (int nt = 0; nt < kN; ++nt)
+#pragma unroll
+          for (int i = 0; i < kChains; ++i) sc[nt][i][0] = sc[nt][i][1] = sc[nt][i][2] = sc[nt][i][3] = 0.f;
+#pragma unroll
+        for (int bx = 0; bx < Cfg::kBoxes; ++bx) {
+#pragma unroll
+          for (int half = 0; half < (D == 64 ? 1 : 2); ++half) {
+            uint4 kw[kN];
+#pragma unroll
+            for (int nt = 0; nt < kN; ++nt) {
+              const uint32_t key = nt * 8 + g;
+              uint32_t off;
+              if constexpr (D == 64) off = sw128(key >> 1, (key & 1) * 4 + tq);
+              else off = bx * kKeys * 128 + sw128(key, 2 * tq + half);
+              kw[nt] = *reinterpret_cast<const uint4*>(kt + off);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int kk = bx * 8 + half * 4 + i;
+              uint32_t aq[4];
+              if constexpr (D == 256) {
+                const uint4 u = qfrag[kk * 32 + lane];
+                aq[0] = u.x; aq[1] = u.y; aq[2] = u.z; aq[3] = u.w;
+              } else {
+                aq[0] = qa[kk][0]; aq[1] = qa[kk][1]; aq[2] = qa[kk][2]; aq[3] = qa[kk][3];
+              }
+#pragma unroll
+              for (int nt = 0; nt < kN; ++nt) {
+                const uint32_t w = i == 0 ? kw[nt].x : (i == 1 ? kw[nt].y : (i == 2 ? kw[nt].z : kw[nt].w));
+                uint32_t b0, b1;
+                codes_to_half<kE4M3>(w, b0, b1);
+                mma_16816<__half>(sc[nt][i % kChains], aq, b0, b1);
+              }
+            }
+          }
         }
-      } else {
+        __syncwarp();  // the whole warp has read this load
+        if (lane == 0 && uk + Cfg::kStages < nloads) load(uk + Cfg::kStages, st_k, &tmK, 0, full_k);
+        ++uk;
+        if (++st_k == Cfg::kStages) {
+          st_k = 0;
+          phase_k ^= 1u;
+        }
 #pragma unroll
-        for (int gr = 0; gr < kKeys / 16; ++gr)
-          if (key1 + 16 * gr < s1) {
-            const int at = ld * (kKeys / 16) + gr;
-            add_values(vt, gr, pa[at], pl[kSplit ? at : 0], s1 - key1 - 16 * gr, std::true_type{});
+        for (int nt = 0; nt < kN; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            s[ld * kN + nt][e] = sc[nt][0][e];
+            if constexpr (kChains == 2) s[ld * kN + nt][e] += sc[nt][1][e];
           }
       }
-      __syncwarp();  // the whole warp has read this load
-      if (lane == 0 && uv + Cfg::kStages < nloads) load(uv + Cfg::kStages, st_v, &tmV, 1, full_v);
-      ++uv;
-      if (++st_v == Cfg::kStages) {
-        st_v = 0;
-        phase_v ^= 1u;
+      if (!ok) break;
+
+      // ---- softmax (exp2 domain), rows g and g + 8
+      const bool masked = key0 + kTileKeys > safe_end;  // the same for the whole warp
+      if (masked) {
+#pragma unroll
+        for (int nt = 0; nt < kNt; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2 * kHalves; ++e)
+            if (key0 + nt * 8 + 2 * tq + (e & 1) >= row_end[e >> 1]) s[nt][e] = -INFINITY;
+      }
+      if constexpr (kLogits) {
+        // up to 16-key alignment the slots behind the last key are this warp's too
+        // (nothing reads them); the capacity is a multiple of 16
+#pragma unroll
+        for (int hr = 0; hr < kHalves; ++hr) {
+          if (lrow[hr] != nullptr) {
+#pragma unroll
+            for (int nt = 0; nt < kNt; ++nt)
+              if (key0 + nt / 2 * 16 < s1) {
+                const float sa = s[nt][2 * hr], sb = s[nt][2 * hr + 1], fx = f[hr][nt / 2];
+                *reinterpret_cast<float2*>(lrow[hr] + key0 + nt * 8 + 2 * tq) =
+                    make_float2(masked && sa == -INFINITY ? sa : sa * fx, masked && sb == -INFINITY ? sb : sb * fx);
+              }
+          }
+        }
+      }
+      float mx[kHalves], vx[kHalves];  // this lane's largest x, largest x + log2 vs
+#pragma unroll
+      for (int hr = 0; hr < kHalves; ++hr) {
+#pragma unroll
+        for (int gr = 0; gr < Cfg::kGroups; ++gr) {
+          const float top = fmaxf(fmax3(s[2 * gr][2 * hr], s[2 * gr][2 * hr + 1], s[2 * gr + 1][2 * hr]),
+                                  s[2 * gr + 1][2 * hr + 1]) * f[hr][gr];
+          mx[hr] = gr == 0 ? top : fmaxf(mx[hr], top);
+          vx[hr] = gr == 0 ? top + lv[gr] : fmaxf(vx[hr], top + lv[gr]);
+        }
+      }
+      bool above = false;
+#pragma unroll
+      for (int hr = 0; hr < kHalves; ++hr) above = above || mx[hr] > m[hr] + kSlack || vx[hr] > mv[hr] + kSlack;
+      if (__any_sync(0xffffffffu, above)) {
+#pragma unroll
+        for (int hr = 0; hr < kHalves; ++hr) {
+#pragma unroll
+          for (int sh = 1; sh < 4; sh <<= 1) {
+            mx[hr] = fmaxf(mx[hr], __shfl_xor_sync(0xffffffffu, mx[hr], sh));
+            vx[hr] = fmaxf(vx[hr], __shfl_xor_sync(0xffffffffu, vx[hr], sh));
+          }
+          const float mn = fmaxf(m[hr], mx[hr]), vn = fmaxf(mv[hr], vx[hr]);
+          lsum[hr] *= ex2_approx(m[hr] - mn);
+          const float al = ex2_approx(mv[hr] - vn);
+          m[hr] = mn;
+          mv[hr] = vn;
+#pragma unroll
+          for (int j = 0; j < Cfg::kTilesN; ++j) {
+            o[j][2 * hr] *= al;
+            o[j][2 * hr + 1] *= al;
+            if constexpr (kLow) {
+              o[j][2] *= al;
+              o[j][3] *= al;
+            }
+          }
+        }
+      }
+      uint32_t pa[Cfg::kGroups][4], pl[kSplit ? Cfg::kGroups : 1][4];
+      if (masked) tile_weights<Cfg::kGroups, kHalves, true, kSplit, kLow>(s, f, lv, m, mv, lsum, pa, pl);
+      else tile_weights<Cfg::kGroups, kHalves, false, kSplit, kLow>(s, f, lv, m, mv, lsum, pa, pl);
+
+      // ---- O += P V
+#pragma unroll
+      for (int ld = 0; ld < Cfg::kLoads; ++ld) {
+        ok = ok && wait(&full_v[st_v], phase_v);
+        if (!ok) continue;
+        const uint32_t vt = smem_u32(ring + st_v * Cfg::kStageBytes + Cfg::kTileBytes);
+        const int key1 = key0 + ld * kKeys;
+        if (key1 + kKeys <= s1) {
+#pragma unroll
+          for (int gr = 0; gr < kKeys / 16; ++gr) {
+            const int at = ld * (kKeys / 16) + gr;
+            add_values(vt, gr, pa[at], pl[kSplit ? at : 0], 16, std::false_type{});
+          }
+        } else {
+#pragma unroll
+          for (int gr = 0; gr < kKeys / 16; ++gr)
+            if (key1 + 16 * gr < s1) {
+              const int at = ld * (kKeys / 16) + gr;
+              add_values(vt, gr, pa[at], pl[kSplit ? at : 0], s1 - key1 - 16 * gr, std::true_type{});
+            }
+        }
+        __syncwarp();  // the whole warp has read this load
+        if (lane == 0 && uv + Cfg::kStages < nloads) load(uv + Cfg::kStages, st_v, &tmV, 1, full_v);
+        ++uv;
+        if (++st_v == Cfg::kStages) {
+          st_v = 0;
+          phase_v ^= 1u;
+        }
+      }
+      if (!ok) break;
+    }
+    if (uv < nloads && lane == 0) {
+      // a wait gave up: let the loads already issued land before the shared memory goes away
+      for (int u = seen + uk; u < seen + min(nloads, uk + Cfg::kStages); ++u)
+        mbar_drain(&full_k[u % Cfg::kStages], (u / Cfg::kStages) & 1, 20000000ull);
+      for (int u = seen + uv; u < seen + min(nloads, uv + Cfg::kStages); ++u)
+        mbar_drain(&full_v[u % Cfg::kStages], (u / Cfg::kStages) & 1, 20000000ull);
+    }
+
+    seen += nloads;
+
+    // ---- combine the four warps' states
+    __syncthreads();
+    if (*abort_flag != 0) return;
+#pragma unroll
+    for (int hr = 0; hr < kHalves; ++hr) {
+      lsum[hr] += __shfl_xor_sync(0xffffffffu, lsum[hr], 1);
+      lsum[hr] += __shfl_xor_sync(0xffffffffu, lsum[hr], 2);
+    }
+    float* cm = reinterpret_cast<float*>(smem);            // [4][16] running max
+    float* cl = cm + kKv8Warps * kKv8Rows;                 // [4][16] sums
+    float* cv = cl + kKv8Warps * kKv8Rows;                 // [4][16] O's units
+    float4* co4 = reinterpret_cast<float4*>(smem + 1024);  // [4][D / 16][2][32]: values 16 c + 4 tq ..+3 of rows g, g + 8
+    if constexpr (kLow) {
+#pragma unroll
+      for (int j = 0; j < Cfg::kTilesN; ++j) {
+        o[j][0] += o[j][2];
+        o[j][1] += o[j][3];
       }
     }
-    if (!ok) break;
-  }
-  if (uv < nloads && lane == 0) {
-    // a wait gave up: let the loads already issued land before the shared memory goes away
-    for (int u = seen + uk; u < seen + min(nloads, uk + Cfg::kStages); ++u)
-      mbar_drain(&full_k[u % Cfg::kStages], (u / Cfg::kStages) & 1, 20000000ull);
-    for (int u = seen + uv; u < seen + min(nloads, uv + Cfg::kStages); ++u)
-      mbar_drain(&full_v[u % Cfg::kStages], (u / Cfg::kStages) & 1, 20000000ull);
-  }
-
-  seen += nloads;
-
-  // ---- combine the four warps' states
-  __syncthreads();
-  if (*abort_flag != 0) return;
+    if (tq == 0) {
 #pragma unroll
-  for (int hr = 0; hr < 2; ++hr) {
-    lsum[hr] += __shfl_xor_sync(0xffffffffu, lsum[hr], 1);
-    lsum[hr] += __shfl_xor_sync(0xffffffffu, lsum[hr], 2);
-  }
-  float* cm = reinterpret_cast<float*>(smem);            // [4][16] running max
-  float* cl = cm + kKv8Warps * kKv8Rows;                 // [4][16] sums
-  float* cv = cl + kKv8Warps * kKv8Rows;                 // [4][16] O's units
-  float4* co4 = reinterpret_cast<float4*>(smem + 1024);  // [4][D / 16][2][32]: values 16 c + 4 tq ..+3 of rows g, g + 8
-  if (tq == 0) {
-#pragma unroll
-    for (int hr = 0; hr < 2; ++hr) {
-      cm[warp * 16 + g + 8 * hr] = m[hr] == kNone ? -INFINITY : m[hr];
-      cl[warp * 16 + g + 8 * hr] = lsum[hr];
-      cv[warp * 16 + g + 8 * hr] = mv[hr] == kNone ? -INFINITY : mv[hr];
-    }
-  }
-#pragma unroll
-  for (int c = 0; c < D / 16; ++c) {
-#pragma unroll
-    for (int hr = 0; hr < 2; ++hr)
-      co4[((warp * (D / 16) + c) * 2 + hr) * 32 + lane] = make_float4(o[2 * c][2 * hr], o[2 * c + 1][2 * hr],
-                                                                     o[2 * c][2 * hr + 1], o[2 * c + 1][2 * hr + 1]);
-  }
-  __syncthreads();
-
-  // Per row: M = max_w m_w, L = sum_w 2^(m_w - M) l_w; O = sum_w 2^(mv_w - M) O_w / L
-  // (2^(mv_w - M) <= the largest vs: finite), LSE = M + log2 L.
-  const int rows_here = min(kKv8Rows, rows_total - rg * kKv8Rows);
-  const int64_t orow0 = (static_cast<int64_t>(b) * a.Hq + static_cast<int64_t>(hkv) * G) * a.Lq +
-                        static_cast<int64_t>(rg) * kKv8Rows;
-  const int64_t slot = (blockIdx.x + static_cast<int64_t>(b) * heads + uh) * kKv8Rows;
-#pragma unroll
-  for (int hr = 0; hr < 2; ++hr) {
-    const int r = g + 8 * hr;
-    if (r >= rows_here) break;
-    float M = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kKv8Warps; ++w) M = fmaxf(M, cm[w * 16 + r]);
-    float L = 0.f, wt[kKv8Warps];
-#pragma unroll
-    for (int w = 0; w < kKv8Warps; ++w) {
-      const float mw = cm[w * 16 + r], vw = cv[w * 16 + r];
-      // a warp whose maximum is -inf saw no key, or only NaN: its sum then says so
-      L += mw == -INFINITY ? cl[w * 16 + r] : ex2_approx(mw - M) * cl[w * 16 + r];
-      wt[w] = vw == -INFINITY ? 0.f : ex2_approx(vw - (M == -INFINITY ? 0.f : M));
-    }
-    const float inv = L == 0.f ? 0.f : 1.0f / L;
-#pragma unroll
-    for (int w = 0; w < kKv8Warps; ++w) wt[w] *= inv;
-    if (warp == 0 && tq == 0) {
-      const float lse = L == 0.f ? -INFINITY : M + __log2f(L);
-      if (whole_unit) {
-        if (a.lse != nullptr) a.lse[orow0 + r] = lse;
-      } else {
-        // a NaN partial is handed on as +inf: the merge's maximum would drop a
-        // NaN and take the row for empty, while 2^(inf - inf) keeps it
-        a.part_lse[slot + r] = isnan(lse) ? INFINITY : lse;
+      for (int hr = 0; hr < kHalves; ++hr) {
+        cm[warp * 16 + g + 8 * hr] = m[hr] == kNone ? -INFINITY : m[hr];
+        cl[warp * 16 + g + 8 * hr] = lsum[hr];
+        cv[warp * 16 + g + 8 * hr] = mv[hr] == kNone ? -INFINITY : mv[hr];
       }
     }
 #pragma unroll
-    for (int k = 0; k < D / 16 / kKv8Warps; ++k) {
-      const int c = warp + kKv8Warps * k;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = 0; c < D / 16; ++c) {
+#pragma unroll
+      for (int hr = 0; hr < kHalves; ++hr)
+        co4[((warp * (D / 16) + c) * 2 + hr) * 32 + lane] = make_float4(o[2 * c][2 * hr], o[2 * c + 1][2 * hr],
+                                                                       o[2 * c][2 * hr + 1], o[2 * c + 1][2 * hr + 1]);
+    }
+    __syncthreads();
+
+    // Per row: M = max_w m_w, L = sum_w 2^(m_w - M) l_w; O = sum_w 2^(mv_w - M) O_w / L
+    // (2^(mv_w - M) <= the largest vs: finite), LSE = M + log2 L.
+    const int rows_here = min(kKv8Rows, rows_total - rg * kKv8Rows);
+    const int64_t orow0 = (static_cast<int64_t>(b) * a.Hq + static_cast<int64_t>(hkv) * G) * a.Lq +
+                          static_cast<int64_t>(rg) * kKv8Rows;
+    const int64_t slot = (blockIdx.x + static_cast<int64_t>(b) * heads + uh) * kKv8Rows;
+#pragma unroll
+    for (int hr = 0; hr < kHalves; ++hr) {
+      const int r = g + 8 * hr;
+      if (r >= rows_here) break;
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kKv8Warps; ++w) M = fmaxf(M, cm[w * 16 + r]);
+      float L = 0.f, wt[kKv8Warps];
 #pragma unroll
       for (int w = 0; w < kKv8Warps; ++w) {
-        const float4 v = co4[((w * (D / 16) + c) * 2 + hr) * 32 + lane];
-        acc.x = fmaf(wt[w], v.x, acc.x);
-        acc.y = fmaf(wt[w], v.y, acc.y);
-        acc.z = fmaf(wt[w], v.z, acc.z);
-        acc.w = fmaf(wt[w], v.w, acc.w);
+        const float mw = cm[w * 16 + r], vw = cv[w * 16 + r];
+        // a warp whose maximum is -inf saw no key, or only NaN: its sum then says so
+        L += mw == -INFINITY ? cl[w * 16 + r] : ex2_approx(mw - M) * cl[w * 16 + r];
+        wt[w] = vw == -INFINITY ? 0.f : ex2_approx(vw - (M == -INFINITY ? 0.f : M));
       }
-      const int d = 16 * c + 4 * tq;
-      if (whole_unit)
-        *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (orow0 + r) * D + d) =
-            make_uint2(pack2<T>(acc.x, acc.y), pack2<T>(acc.z, acc.w));
-      else
-        *reinterpret_cast<float4*>(a.part_o + (slot + r) * D + d) = acc;
+      const float inv = L == 0.f ? 0.f : 1.0f / L;
+#pragma unroll
+      for (int w = 0; w < kKv8Warps; ++w) wt[w] *= inv;
+      if (warp == 0 && tq == 0) {
+        const float lse = L == 0.f ? -INFINITY : M + __log2f(L);
+        if (whole_unit) {
+          if (a.lse != nullptr) a.lse[orow0 + r] = lse;
+        } else {
+          // a NaN partial is handed on as +inf: the merge's maximum would drop a
+          // NaN and take the row for empty, while 2^(inf - inf) keeps it
+          a.part_lse[slot + r] = isnan(lse) ? INFINITY : lse;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < D / 16 / kKv8Warps; ++k) {
+        const int c = warp + kKv8Warps * k;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kKv8Warps; ++w) {
+          const float4 v = co4[((w * (D / 16) + c) * 2 + hr) * 32 + lane];
+          acc.x = fmaf(wt[w], v.x, acc.x);
+          acc.y = fmaf(wt[w], v.y, acc.y);
+          acc.z = fmaf(wt[w], v.z, acc.z);
+          acc.w = fmaf(wt[w], v.w, acc.w);
+        }
+        const int d = 16 * c + 4 * tq;
+        if (whole_unit)
+          *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (orow0 + r) * D + d) =
+              make_uint2(pack2<T>(acc.x, acc.y), pack2<T>(acc.z, acc.w));
+        else
+          *reinterpret_cast<float4*>(a.part_o + (slot + r) * D + d) = acc;
+      }
     }
-  }
-  // the next segment's loads may overwrite what the combine has just read and written
-  fence_proxy_async_smem();
-  __syncthreads();
+    // the next segment's loads may overwrite what the combine has just read and written
+    fence_proxy_async_smem();
+    __syncthreads();
   }
 }
 

@@ -176,11 +176,11 @@ int encode_codes(CUtensorMap* m, const void* base, int64_t tokens, int D) {
   return r == CUDA_SUCCESS ? 0 : static_cast<int>(cudaErrorInvalidValue);
 }
 
-template <int D, typename T, bool kE4M3, bool kLogits>
+template <int D, typename T, bool kE4M3, bool kLogits, int kHalves>
 int launch_decode_kv8(const CUtensorMap& tk, const CUtensorMap& tv, const Kv8DecodeArgs& a, dim3 grid,
                       skv_stream_t st) {
   using Cfg = Kv8DecodeCfg<D>;
-  auto kern = decode_kv8_kernel<D, T, kE4M3, kLogits>;
+  auto kern = decode_kv8_kernel<D, T, kE4M3, kLogits, kHalves>;
   static std::atomic<uint64_t> ready{0};  // devices (below 64) the limit is set on
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -194,14 +194,21 @@ int launch_decode_kv8(const CUtensorMap& tk, const CUtensorMap& tv, const Kv8Dec
   return launch(kern, grid, kKv8Threads, Cfg::kSmemBytes, st, 1, tk, tv, a);
 }
 
+template <int D, typename T, int kHalves>
+int launch_decode_kv8_h(const CUtensorMap& tk, const CUtensorMap& tv, const Kv8DecodeArgs& a, skv_code codes,
+                        dim3 grid, skv_stream_t st) {
+  if (codes == SKV_E4M3)
+    return a.logits ? launch_decode_kv8<D, T, true, true, kHalves>(tk, tv, a, grid, st)
+                    : launch_decode_kv8<D, T, true, false, kHalves>(tk, tv, a, grid, st);
+  return a.logits ? launch_decode_kv8<D, T, false, true, kHalves>(tk, tv, a, grid, st)
+                  : launch_decode_kv8<D, T, false, false, kHalves>(tk, tv, a, grid, st);
+}
+
 template <int D, typename T>
 int launch_decode_kv8_d(const CUtensorMap& tk, const CUtensorMap& tv, const Kv8DecodeArgs& a, skv_code codes,
                         dim3 grid, skv_stream_t st) {
-  if (codes == SKV_E4M3)
-    return a.logits ? launch_decode_kv8<D, T, true, true>(tk, tv, a, grid, st)
-                    : launch_decode_kv8<D, T, true, false>(tk, tv, a, grid, st);
-  return a.logits ? launch_decode_kv8<D, T, false, true>(tk, tv, a, grid, st)
-                  : launch_decode_kv8<D, T, false, false>(tk, tv, a, grid, st);
+  return a.Hq / a.Hkv * a.Lq <= kKv8Rows / 2 ? launch_decode_kv8_h<D, T, 1>(tk, tv, a, codes, grid, st)
+                                             : launch_decode_kv8_h<D, T, 2>(tk, tv, a, codes, grid, st);
 }
 
 // keys of a tile of the division among CTAs
