@@ -6,7 +6,7 @@
 // partial (O, LSE) that kv8_merge_kernel joins.  (Equal splits of each sequence
 // left SMs idle where lengths differ or units do not divide the SMs: B = 16, 16
 // heads, D = 64, lengths 4096 to 16384: 89 us with one split, 74 with the best,
-// 65 so.)
+// 65 so, all without the keys' weights.)
 //
 // With code blocks of scales ks, vs (one per block of tokens and head):
 //   x_j = scale * log2(e) * ks_j * (q . ck_j),  p_j = 2^(x_j - m),  m = max x_j
@@ -21,10 +21,17 @@
 // fp16 weights use their range however much the scales of V differ.  Both
 // references follow the maxima loosely (within a factor of 2^8).
 //
-// What bounds it: bytes.  At HBM rate an SM receives about 23 codes per clock;
-// turning them into fp16 costs 1.25 (K) and 1.5 (V) lane instructions each,
-// about a quarter of the issue slots, and the 16 rows' MMAs about as much
-// again, so mma.sync keeps pace (tcgen05 would want 128 rows).
+// What bounds it: bytes, and next the turning of codes into fp16.  At HBM rate an
+// SM receives about 23 codes per clock; turning them costs 1.25 (K) and 1.5 (V)
+// lane instructions each for int8, less for e4m3, about a quarter of the issue
+// slots, and the 16 rows' MMAs about as much again, so mma.sync nearly keeps pace
+// (tcgen05 would want 128 rows).  Whole calls, bf16 q, one row a head (a copy
+// reaches 6.6 TB/s):
+//   D = 64,  B = 16, 16 / 16 heads, 16384 keys: e4m3 87.0 us (6.2 TB/s), int8 100.4 (5.4)
+//   D = 128, B = 2, 32 / 8 heads, 32768 keys:   e4m3 27.3 us (4.9 TB/s), int8 30.8 (4.4)
+//   D = 256, B = 1, 16 / 4 heads, 131072 keys:  e4m3 50.6 us (5.3 TB/s), int8 57.7 (4.7)
+//   D = 128, B = 1, 32 / 8 heads, 4096 keys:    e4m3 8.5 us, int8 9.0: latency
+// Of these about 5 us are the start, the four warps' combine and the merge launch.
 //
 // Layout: the order of a product's summands is free as long as both operands
 // agree, so of a key row a thread takes the 32 contiguous codes at 32 (lane & 3)
@@ -837,9 +844,10 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
 }
 
 // Joins the partials of each row whose unit is divided: parts c0 + u .. c1 + u of
-// unit u, one CTA for 64 values of a row, its threads over columns and parts (a
-// whole row of 256 left each thread 18 of 74 parts: 5 us instead of 2).  M = max_p L_p,
-// w_p = 2^(L_p - M), O = sum w_p O_p / sum w_p, LSE = M + log2 sum w_p.
+// unit u, M = max_p L_p, w_p = 2^(L_p - M), O = sum w_p O_p / sum w_p, LSE = M +
+// log2 sum w_p.  One CTA takes 64 values of a row, its threads over columns and
+// parts (a whole row of 256 left each thread 18 of 74 parts: 5 us instead of 2).
+// Bound by latency: a launch, the LSEs, a few rounds of parts.
 constexpr int kKv8MaxCtas = 1024;
 
 template <int D, typename T>
@@ -949,10 +957,11 @@ __global__ void __launch_bounds__(256) kv8_merge_kernel(const Kv8DecodeArgs a, i
 // Attention weights of the keys: weights[b, h, j] += sum over the rows of kv
 // head h of 2^(x_j - LSE), from the logits the split kernel left and the merged
 // LSE (rows that see no key add nothing).  Bound by bytes: 4 per row and key,
-// most of them still in L2, and 8 per key.  A thread takes 4 keys, and kRows rows at
-// a time in flight: 8, or 2 where a head has no more (more threads to an SM: one
-// row, 16 heads, B = 16, 10000 keys: 79 us of decode against 84; with 16 rows, 8 are
-// 44 against 46).
+// most of them still in L2, and 8 per key; with the logits' stores it adds 11 us
+// to 31 us of decode (B = 2, 8 kv heads, 16 rows each, 32768 keys, int8).  A thread
+// takes 4 keys, and kRows rows at a time in flight: 8, or 2 where a head has no
+// more (more threads to an SM: one row, 16 heads, B = 16, 10000 keys: 79 us of
+// decode against 84; with 16 rows, 8 are 44 against 46).
 struct Kv8WeightArgs {
   const float* logits;   // [B, Hkv, rows, capacity]
   const float* lse;      // [B, Hkv, rows]

