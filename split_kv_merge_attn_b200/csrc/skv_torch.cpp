@@ -13,6 +13,7 @@
 
 #include <ATen/ATen.h>
 #include <ATen/cuda/CUDAContext.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -155,8 +156,9 @@ class On {
   std::optional<c10::cuda::CUDAStreamGuard> stream_;
 };
 
+// (not through the operator dispatch of at::empty)
 at::Tensor empty(at::IntArrayRef shape, at::ScalarType dt, int dev) {
-  return at::empty(shape, at::TensorOptions().dtype(dt).device(at::kCUDA, static_cast<c10::DeviceIndex>(dev)));
+  return at::Tensor(at::detail::empty_cuda(shape, dt, at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(dev)), std::nullopt));
 }
 
 // ------------------------------------------------------------ the cache
