@@ -12,13 +12,15 @@
 // themselves are always finite.
 //
 // Bound by bytes (16 bits in, 8 out).  One CTA takes 128 tokens of one
-// (batch entry, head) of K or of V, each of its warps 16 of them (8 at D = 256),
+// (batch entry, head) of K or of V (of both at D = 64), each of its warps 16 of them (8 at D = 256),
 // which it holds in registers between the maximum and the codes: one read, one
 // write.  Every block size (16, 32, 64, 128) is then a whole number of warps.
-// 4 sequences of 8192 tokens, bf16, 201 MB in and out: 38.4 us at D = 128 with 8 heads
-// (5.2 TB/s), 50 us at D = 64 with 16 (4.0), 44 us at D = 256 with 4 (4.6).  What is
-// missing is the chain of a CTA (start, values, maximum, codes) at the CTAs that
+// 4 sequences of 8192 tokens, bf16, 201 MB in and out: 39.6 us at D = 128 with 8 heads
+// (5.1 TB/s), 43.6 us at D = 64 with 16 (4.6), 44.5 us at D = 256 with 4 (4.5).  What
+// is missing is the chain of a CTA (start, values, maximum, codes) at the CTAs that
 // registers allow; fewer instructions (packed products and sums) changed nothing.
+// The addresses of the codes are formed behind the loads of the values: ahead of them
+// a token each of 32 sequences took 0.5 us longer, long prompts 0.6 less.
 #pragma once
 
 #include "skv_device.cuh"
@@ -28,6 +30,10 @@ namespace skv {
 constexpr int kKv8Window = 128;   // tokens per append CTA
 template <int D>
 constexpr int kAppendThreads = D == 256 ? 512 : 256;
+// K and V of a CTA: both at D = 64, whose rows leave registers for it (43.6 us against
+// 50.0 for 4 sequences of 8192 tokens, 16 heads), one of them above.
+template <int D>
+constexpr int kAppendSides = D == 64 ? 2 : 1;
 constexpr float kKv8TinyScale = 1.17549435e-38f;  // 2^-126
 
 template <bool kE4M3>
@@ -96,18 +102,20 @@ struct Kv8AppendArgs {
 };
 
 template <int D, typename T, bool kE4M3>
-__global__ void __launch_bounds__(kAppendThreads<D>, D == 64 ? 5 : (D == 128 ? 4 : 2)) kv8_append_kernel(const Kv8AppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads<D>, D == 256 ? 2 : 4)
+    kv8_append_kernel(const Kv8AppendArgs a) {
   using Code = Kv8Code<kE4M3>;
   constexpr int kLanes = D / 8;            // lanes of one row, 8 values each
   constexpr int kRows = 32 / kLanes;       // rows a warp takes at once
   constexpr int kWarps = kAppendThreads<D> / 32;
   constexpr int kTokens = kKv8Window / kWarps;  // of a warp
   constexpr int kPasses = kTokens / kRows;
+  constexpr int kSides = kAppendSides<D>;  // K and V, or one of them
   // a programmatic dependent of the kernel before it: waits before any load
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // heads beside each other: in token-major rows they share DRAM pages
-  const int b = blockIdx.y, h = blockIdx.x % a.Hkv, which = blockIdx.z;
+  const int b = blockIdx.y, h = blockIdx.x % a.Hkv, side0 = blockIdx.z;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int start = min(max(a.start[b], 0), a.capacity);
   int count = a.S, first_row = 0;
@@ -131,80 +139,94 @@ __global__ void __launch_bounds__(kAppendThreads<D>, D == 64 ? 5 : (D == 128 ? 4
   const bool touched = block_pos < end && block_pos + a.block > start;
   const bool has_old = touched && block_pos < start;  // older tokens, with a scale of their own
   const bool whole = wpos >= start && wpos + kTokens <= end;  // new rows only
-  const int64_t at = (static_cast<int64_t>(b) * a.Hkv + h) * (a.capacity / a.block) + block_pos / a.block;
-  const float s_old = has_old ? a.scale[which][at] : 0.f;
+  const uint32_t at = (static_cast<uint32_t>(b) * a.Hkv + h) * (a.capacity / a.block) + block_pos / a.block;
+  float s_old[kSides];
+#pragma unroll
+  for (int d = 0; d < kSides; ++d) s_old[d] = has_old ? a.scale[side0 + d][at] : 0.f;
   // rows of token i: row0 + i * step
   const int64_t step = (a.cu != nullptr || a.token_major) ? a.Hkv : 1;
   const int64_t row0 = a.cu != nullptr ? static_cast<int64_t>(first_row) * a.Hkv + h
                        : a.token_major ? static_cast<int64_t>(b) * a.S * a.Hkv + h
                                        : (static_cast<int64_t>(b) * a.Hkv + h) * a.S;
-  const T* src = static_cast<const T*>(a.x[which]) + (row0 + (pos0 - start) * step) * D + cl * 8;
-  const int64_t src_pass = step * kRows * D;
-  uint8_t* codes = a.codes[which] + ((static_cast<int64_t>(b) * a.Hkv + h) * a.capacity + pos0) * D + cl * 8;
+  const int64_t src0 = (row0 + (pos0 - start) * step) * D + cl * 8, src_pass = step * kRows * D;
+  // (a cache has less than 2^31 tokens)
+  const uint32_t token = (static_cast<uint32_t>(b) * a.Hkv + h) * a.capacity + pos0;
+  auto codes_of = [&](int d) { return a.codes[side0 + d] + static_cast<uint64_t>(token) * D + cl * 8; };
   // a lane's rows: new values, or (first block only) the codes of older tokens
-  uint4 v[kPasses];
-  uint32_t top = 0;  // largest magnitude bits of the new values, two 16-bit halves
-  if (whole) {
+  uint4 v[kSides][kPasses];
 #pragma unroll
-    for (int p = 0; p < kPasses; ++p) v[p] = __ldg(reinterpret_cast<const uint4*>(src + p * src_pass));
-  } else {
+  for (int d = 0; d < kSides; ++d) {
+    const T* src = static_cast<const T*>(a.x[side0 + d]) + src0;
+    if (whole) {
 #pragma unroll
-    for (int p = 0; p < kPasses; ++p) {
-      const int pos = pos0 + kRows * p;
-      v[p] = make_uint4(0, 0, 0, 0);
-      if (pos >= start && pos < end) {
-        v[p] = __ldg(reinterpret_cast<const uint4*>(src + p * src_pass));
-      } else if (has_old && pos < start) {
-        const uint2 w = *reinterpret_cast<const uint2*>(codes + kRows * p * D);
-        v[p].x = w.x;
-        v[p].y = w.y;
+      for (int p = 0; p < kPasses; ++p) v[d][p] = __ldg(reinterpret_cast<const uint4*>(src + p * src_pass));
+    } else {
+#pragma unroll
+      for (int p = 0; p < kPasses; ++p) {
+        const int pos = pos0 + kRows * p;
+        v[d][p] = make_uint4(0, 0, 0, 0);
+        if (pos >= start && pos < end) {
+          v[d][p] = __ldg(reinterpret_cast<const uint4*>(src + p * src_pass));
+        } else if (has_old && pos < start) {
+          const uint2 w = *reinterpret_cast<const uint2*>(codes_of(d) + kRows * p * D);
+          v[d][p].x = w.x;
+          v[d][p].y = w.y;
+        }
       }
     }
   }
+  __shared__ uint32_t warp_top[kSides][kWarps];
 #pragma unroll
-  for (int p = 0; p < kPasses; ++p) {
-    // magnitude bits of 16-bit floats order as whole numbers, NaN above infinity
-    const uint32_t t = __vmaxu2(__vmaxu2(v[p].x & 0x7fff7fffu, v[p].y & 0x7fff7fffu),
-                                __vmaxu2(v[p].z & 0x7fff7fffu, v[p].w & 0x7fff7fffu));
-    if (whole || pos0 + kRows * p >= start) top = __vmaxu2(top, t);
+  for (int d = 0; d < kSides; ++d) {
+    uint32_t top = 0;  // largest magnitude bits of the new values, two 16-bit halves
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+      // magnitude bits of 16-bit floats order as whole numbers, NaN above infinity
+      const uint32_t t = __vmaxu2(__vmaxu2(v[d][p].x & 0x7fff7fffu, v[d][p].y & 0x7fff7fffu),
+                                  __vmaxu2(v[d][p].z & 0x7fff7fffu, v[d][p].w & 0x7fff7fffu));
+      if (whole || pos0 + kRows * p >= start) top = __vmaxu2(top, t);
+    }
+    top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+    if (lane == 0) warp_top[d][warp] = top;
   }
-  top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
-
-  __shared__ uint32_t warp_top[kWarps];
-  if (lane == 0) warp_top[warp] = top;
   __syncthreads();  // also orders every read of the old scale before its new value is written
   if (!touched) return;
-  for (int w = group * per; w < (group + 1) * per; ++w) top = max(top, warp_top[w]);
-  const float amax = unpack2<T>(top).x;
-  const float fresh = __fdiv_rn(amax, Code::kMax);
-  float s = (fresh > s_old || isnan(fresh)) ? fresh : s_old;
-  if (s < kKv8TinyScale) s = 0.f;
-  const bool poisoned = !(s < INFINITY);
-  const float inv = kv8_inverse(s);
-  if (warp == group * per && lane == 0) a.scale[which][at] = s;
+#pragma unroll
+  for (int d = 0; d < kSides; ++d) {
+    uint32_t top = 0;
+    for (int w = group * per; w < (group + 1) * per; ++w) top = max(top, warp_top[d][w]);
+    const float amax = unpack2<T>(top).x;
+    const float fresh = __fdiv_rn(amax, Code::kMax);
+    float s = (fresh > s_old[d] || isnan(fresh)) ? fresh : s_old[d];
+    if (s < kKv8TinyScale) s = 0.f;
+    const bool poisoned = !(s < INFINITY);
+    const float inv = kv8_inverse(s);
+    if (warp == group * per && lane == 0) a.scale[side0 + d][at] = s;
 
-  const uint64_t inv2 = f2_pack(inv, inv);
-  auto encode = [&](const uint4& x) {
-    uint2 w;
-    w.x = Code::encode4(unpack2<T>(x.x), unpack2<T>(x.y), inv2);
-    w.y = Code::encode4(unpack2<T>(x.z), unpack2<T>(x.w), inv2);
-    return w;
-  };
-  if (whole && !poisoned) {
+    uint8_t* codes = codes_of(d);
+    const uint64_t inv2 = f2_pack(inv, inv);
+    auto encode = [&](const uint4& x) {
+      uint2 w;
+      w.x = Code::encode4(unpack2<T>(x.x), unpack2<T>(x.y), inv2);
+      w.y = Code::encode4(unpack2<T>(x.z), unpack2<T>(x.w), inv2);
+      return w;
+    };
+    if (whole && !poisoned) {
 #pragma unroll
-    for (int p = 0; p < kPasses; ++p) *reinterpret_cast<uint2*>(codes + kRows * p * D) = encode(v[p]);
-    return;
-  }
-  const bool wider = s > s_old || (poisoned && s_old < INFINITY);
+      for (int p = 0; p < kPasses; ++p) *reinterpret_cast<uint2*>(codes + kRows * p * D) = encode(v[d][p]);
+      continue;
+    }
+    const bool wider = s > s_old[d] || (poisoned && s_old[d] < INFINITY);
 #pragma unroll
-  for (int p = 0; p < kPasses; ++p) {
-    const int pos = pos0 + kRows * p;
-    if (pos >= end || (pos < start && !wider)) continue;
-    uint2 w = make_uint2(0, 0);
-    if (!poisoned)
-      w = pos >= start ? encode(v[p])
-                       : make_uint2(Code::recode4(v[p].x, s_old, inv2), Code::recode4(v[p].y, s_old, inv2));
-    *reinterpret_cast<uint2*>(codes + kRows * p * D) = w;
+    for (int p = 0; p < kPasses; ++p) {
+      const int pos = pos0 + kRows * p;
+      if (pos >= end || (pos < start && !wider)) continue;
+      uint2 w = make_uint2(0, 0);
+      if (!poisoned)
+        w = pos >= start ? encode(v[d][p])
+                         : make_uint2(Code::recode4(v[d][p].x, s_old[d], inv2), Code::recode4(v[d][p].y, s_old[d], inv2));
+      *reinterpret_cast<uint2*>(codes + kRows * p * D) = w;
+    }
   }
 }
 

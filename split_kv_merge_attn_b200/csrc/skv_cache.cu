@@ -420,7 +420,7 @@ skv_status kv8_append(const void* k_new, const void* v_new, void* k_codes, void*
   const int64_t windows = std::min<int64_t>((static_cast<int64_t>(S) + kKv8Window - 2) / kKv8Window + 1,
                                             ceil_div64(capacity, kKv8Window));
   if (windows * Hkv > 0x7fffffff) return SKV_ERR_UNSUPPORTED;
-  const dim3 grid(static_cast<unsigned>(windows * Hkv), static_cast<unsigned>(B), 2);
+  const dim3 grid(static_cast<unsigned>(windows * Hkv), static_cast<unsigned>(B), D == 64 ? 2 / kAppendSides<64> : 2);
   return cuda_status(dtype == SKV_BF16 ? launch_append_d<__nv_bfloat16>(a, D, codes, grid, stream)
                                        : launch_append_d<__half>(a, D, codes, grid, stream));
 }
