@@ -479,7 +479,8 @@ skv_status kv8_fetch(const void* k_codes, const void* v_codes, const float* k_sc
  * per entry and call; entries >= kv_len[b] stay as they are.
  * workspace: device, 256-byte aligned, >= attn_splitkv_kv8_workspace(...) bytes
  * for the CTA count used (with weights it holds the rows' logits, 4 * B * Hq * Lq *
- * capacity bytes).  Nothing in it needs to start at zero. */
+ * capacity bytes).  Nothing in it needs to start at zero.  Calls that may run at
+ * the same time need workspaces of their own, and so do their weights. */
 skv_status attn_splitkv_decode_kv8(const void* q, const void* k_codes, const void* v_codes, const float* k_scale,
                                    const float* v_scale, void* out, float* lse, float* weights, int B, int Hq, int Hkv,
                                    int Lq, int capacity, int D, int block, float scale, skv_dtype dtype,

@@ -119,3 +119,56 @@ def test_readme_step_runs():
     # with max|q| < 5 and |k| 0.8 on average: y < 66, 3.6e-4
     total = env["weights"].sum(-1)
     assert torch.allclose(total, torch.full_like(total, 160.0), rtol=3.6e-4)
+
+
+def test_a_cache_beyond_32_bit_offsets():
+    """Three heads of 2^23 tokens of 256 codes: byte offsets above 2^32, within and
+    between heads.  K scales of 0 make every logit 0, so LSE = log2 n, O the mean of V
+    and each weight G / n; V scales are 0 but for the last block.  An O is off by half a
+    bf16 step and 2^-10 of sum p |v| (2^-11 of a weight's fp16 rounding, as much again
+    for fp32 sums and the merge); LSE by 2^-17, weights by twice that (relative)."""
+    H, G, n, D, block = 3, 2, 1 << 23, 256, 64
+    cache = skv.kv8_cache(1, H, n, D, block)  # int8: any byte is a finite code
+    cache.k_scale.zero_()
+    cache.v_scale.zero_()
+    g = gen(2)
+    k, v = (torch.randn(1, H, 100, D, generator=g).bfloat16().cuda() for _ in range(2))
+    small = skv.kv8_cache(1, H, 128, D, block)
+    small.k_scale.zero_()
+    small.v_scale.zero_()
+    skv.kv8_append(cache, k, v, i32([n - 100]))
+    skv.kv8_append(small, k, v, i32([28]))
+    for t, s in zip(cache, small):  # the same blocks, seen from the end
+        assert torch.equal(t[:, :, t.shape[2] - (100 if t.dtype == torch.int8 else 2):],
+                           s[:, :, 28 if t.dtype == torch.int8 else 0:])
+    far, near = (skv.kv8_fetch(c, 100, start=i32([at])) for c, at in ((cache, n - 100), (small, 28)))
+    assert torch.equal(far[0], near[0]) and torch.equal(far[1], near[1])
+
+    cache.k_scale.zero_()
+    cache.v_scale[:, :, :-1] = 0
+    cache.v_scale[:, :, -1] = n / 1024
+    q = torch.randn(1, G * H, 1, D, generator=g).bfloat16().cuda()
+    weights = torch.zeros(1, H, n, device="cuda")
+    out, lse = skv.attn_splitkv_decode_kv8(q, cache, weights=weights)
+    want = cache.v[:, :, -block:].double().sum(2) / 1024
+    size = cache.v[:, :, -block:].double().abs().sum(2) / 1024
+    off = (out[:, :, 0].view(1, H, G, D).double() - want[:, :, None]).abs()
+    assert (off <= 2.0 ** -8 * want.abs()[:, :, None] + 2.0 ** -10 * size[:, :, None]).all()
+    assert (lse - 23).abs().max() <= 2.0 ** -17
+    assert (weights * (n / G) - 1).abs().max() <= 2.0 ** -16
+
+    cache.k_scale.fill_(0.5)
+    cache.v_scale.fill_(0.25)
+    weights.zero_()
+    weights[:, :, n - 600 : n - 100] = 1 + torch.rand(1, H, 500, generator=g).cuda()
+    to, to_weights = skv.kv8_cache(1, H, 512, D, block), torch.zeros(1, H, 512, device="cuda")
+    kept, new_len = skv.kv8_evict(cache, to, weights, to_weights, None, 500, sink=3, recent=100)
+    assert new_len.tolist() == [500]
+    for h in range(H):
+        w = weights[0, h, n - 600 : n - 100].tolist()
+        order = sorted(range(500), key=lambda j: (-w[j], j))[:397]
+        at = [0, 1, 2] + sorted(n - 600 + j for j in order) + list(range(n - 100, n))
+        assert kept[0, h].tolist() == at
+        at = torch.tensor(at, device="cuda")
+        assert torch.equal(to.k[0, h, :500], cache.k[0, h, at]) and torch.equal(to.v[0, h, :500], cache.v[0, h, at])
+        assert torch.equal(to_weights[0, h, :500], weights[0, h, at])
