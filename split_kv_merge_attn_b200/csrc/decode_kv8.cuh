@@ -506,14 +506,15 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
 #pragma unroll
     for (int j = 0; j < Cfg::kTilesN; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
 
-    // Weights of fp16 rounding (2^-11) vanish under a bf16 output's (2^-8); beside an
-    // fp16 output's they made the error 1.2 to 1.6 times that of rounding the output
-    // alone.  There a weight is two fp16 numbers (2^-22): of at most 8 rows, the second
-    // in rows 8-15, at no MMA (the whole call, B = 16, 16 heads, D = 64, 16384 keys, e4m3:
-    // 87.7 us against 107 with MMAs of its own and 87.0 for bf16); of 16, with twice
-    // the MMAs of P V (B = 2, 32 / 8 heads, Lq = 4, D = 128, 32768 keys, int8: 37.4 us
-    // against 31.4 for bf16).
-    constexpr bool kLow = std::is_same<T, __half>::value && kHalves == 1;
+    // A weight rounded to fp16 once (2^-11 of it at most) turns about one bf16 output in
+    // sixteen to the other side of a tie and adds 1.2 to 1.6 times an fp16 output's own
+    // rounding.  Of at most 8 rows a weight is two fp16 numbers (2^-22), the second in rows
+    // 8-15, at no MMA (whole calls, bf16, in two numbers against one: B = 16, 16 heads, D =
+    // 64, 16384 keys, e4m3 87.5 us against 87.0, int8 99.0 against 100.7; D = 256, 131072
+    // keys, e4m3 49.7 against 50.7).  Of 16 rows that takes twice the MMAs of P V (B = 2, 32 /
+    // 8 heads, Lq = 4, D = 128, 32768 keys, int8: 37.5 us against 31.6): fp16 outputs have
+    // it, bf16 ones have one number, whose error is an eighth of their half step at most.
+    constexpr bool kLow = kHalves == 1;
     constexpr bool kSplit = std::is_same<T, __half>::value && kHalves == 2;
     constexpr int kNt = kTileKeys / 8;
     // O += P V over one group of 16 keys, nvalid of them before the end

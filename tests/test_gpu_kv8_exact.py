@@ -1,0 +1,46 @@
+"""How exact the 8-bit decode's outputs are, beyond the tolerances of
+test_gpu_kv8_decode.py: what its weights may add to the output's own rounding."""
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+import split_kv_merge_attn_b200 as skv
+from tests._kv8_helpers import DT, filled_cache, gen, i32, values
+from tests.test_gpu_kv8_decode import row_sizes
+
+pytestmark = pytest.mark.gpu
+
+DIGITS = {"bf16": 8, "fp16": 11}  # of the significand
+
+
+def half_step(x, dtype):
+    """Half a rounding step of the output type at x."""
+    return 2.0 ** (np.floor(np.log2(np.maximum(np.abs(x), 2.0 ** -14))) - DIGITS[dtype])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("codes", ["int8", "e4m3"])
+@pytest.mark.parametrize("G,Lq,D", [(1, 1, 64), (4, 1, 128), (4, 2, 128), (2, 1, 256)])
+def test_outputs_of_few_rows_are_those_of_the_exact_weights(G, Lq, D, codes, dtype):
+    """With at most 8 rows a kv head an output is the exact O rounded once, but for what
+    fp32 sums leave: half a step of the output type, plus (2^-21 + r + 2^-16) of sum p |v|,
+    where a weight in two fp16 numbers is off by 2^-22, V's scale in it by as much, r = 2
+    ln 2 (2^-18 y + 2^-17) + 2^-20 bounds its exponent's error (the note of
+    test_gpu_kv8_decode.py), 2^-16 the fp32 sums and merge, and 2^-25 of each code for
+    what lies below fp16's range.  Few keys and small logits, so that a weight rounded
+    to fp16 once (2^-12 of it and more) shows: y < 2, r < 2^-15."""
+    B, Hkv, n, capacity = 16, 8, 5, 64
+    cache = filled_cache(B, Hkv, capacity, D, 16, codes, [n] * B, seed=G + D, scale_span=0.0)
+    q = (0.02 * 128 ** 0.5 / D ** 0.5 * torch.randn(B, G * Hkv, Lq, D, generator=gen(Lq))).to(DT[dtype]).cuda()
+    out, _ = skv.attn_splitkv_decode_kv8(q, cache, kv_len=i32([n] * B))
+    k, v = values(cache.k, cache.k_scale, [n] * B), values(cache.v, cache.v_scale, [n] * B)
+    ref, _ = O.decode(q, k, v, D ** -0.5, kv_len=[n] * B)
+    size, _ = O.decode(q, k, np.abs(v), D ** -0.5, kv_len=[n] * B)
+    y = row_sizes(q, k, D ** -0.5, [n] * B)
+    assert y.max() < 2
+    rel = 2 * np.log(2.0) * (2.0 ** -18 * y + 2.0 ** -17) + 2.0 ** -20
+    codes_max = 127.0 if codes == "int8" else 448.0
+    small = 2.0 ** -25 * n * codes_max * float(cache.v_scale[:, :, 0].max())
+    off = np.abs(O.to_f64(out) - ref) - half_step(ref, dtype) - (2.0 ** -21 + rel + 2.0 ** -16)[..., None] * size - small
+    assert off.max() <= 0, off.max()
