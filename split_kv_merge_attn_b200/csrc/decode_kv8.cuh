@@ -19,7 +19,8 @@
 // P V the weights carry the block's scale: p_j vs_j is kept relative to its own
 // running maximum M >= x_j + log2 vs_j, apart from the softmax's m, so that the
 // fp16 weights use their range however much the scales of V differ.  Both
-// references follow the maxima loosely (within a factor of 2^8).
+// references follow the maxima loosely (within a factor of 2^8), and the weights'
+// lies 2^7 below: they end at 2^15, and what is dropped lies 2^-32 below the heaviest.
 //
 // What bounds it: bytes, and next the turning of codes into fp16.  At HBM rate an
 // SM receives about 23 codes per clock; turning them costs 1.25 (K) and 1.5 (V)
@@ -493,8 +494,11 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
     // m and mv are references a little behind the running maxima of x and of
     // x + log2 vs: they move only when a value lies more than 2^kSlack above, so
     // most tiles need no reduction over a row and no rescaling.  p and the fp16
-    // weights p vs / 2^mv then reach 2^kSlack, far from fp16's limit.
-    constexpr float kSlack = 8.f;
+    // weights p vs / 2^mv, with mv kLift below, then reach 2^(kSlack + kLift): within
+    // fp16's limit, and as far as can be from its smallest step.  (With mv at the maximum
+    // a warp lost the keys 2^-25 below its heaviest: of 2^20 keys of one CTA, 2^-26 each
+    // beside one of 1, a quarter of their sum.)
+    constexpr float kSlack = 8.f, kLift = 7.f;
     constexpr float kNone = -1.0e30f;  // nothing seen yet
     float m[kHalves], mv[kHalves], lsum[kHalves];
 #pragma unroll
@@ -678,7 +682,7 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
       }
       bool above = false;
 #pragma unroll
-      for (int hr = 0; hr < kHalves; ++hr) above = above || mx[hr] > m[hr] + kSlack || vx[hr] > mv[hr] + kSlack;
+      for (int hr = 0; hr < kHalves; ++hr) above = above || mx[hr] > m[hr] + kSlack || vx[hr] > mv[hr] + (kSlack + kLift);
       if (__any_sync(0xffffffffu, above)) {
 #pragma unroll
         for (int hr = 0; hr < kHalves; ++hr) {
@@ -687,7 +691,7 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
             mx[hr] = fmaxf(mx[hr], __shfl_xor_sync(0xffffffffu, mx[hr], sh));
             vx[hr] = fmaxf(vx[hr], __shfl_xor_sync(0xffffffffu, vx[hr], sh));
           }
-          const float mn = fmaxf(m[hr], mx[hr]), vn = fmaxf(mv[hr], vx[hr]);
+          const float mn = fmaxf(m[hr], mx[hr]), vn = fmaxf(mv[hr], vx[hr] - kLift);
           lsum[hr] *= ex2_approx(m[hr] - mn);
           const float al = ex2_approx(mv[hr] - vn);
           m[hr] = mn;

@@ -44,3 +44,33 @@ def test_outputs_of_few_rows_are_those_of_the_exact_weights(G, Lq, D, codes, dty
     small = 2.0 ** -25 * n * codes_max * float(cache.v_scale[:, :, 0].max())
     off = np.abs(O.to_f64(out) - ref) - half_step(ref, dtype) - (2.0 ** -21 + rel + 2.0 ** -16)[..., None] * size - small
     assert off.max() <= 0, off.max()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("D,rows", [(64, 1), (128, 1), (64, 16)])
+def test_many_light_keys_beside_a_heavy_one(D, rows, dtype):
+    """2^20 keys in one CTA, 2^-26 of a heavy one each, whose value is 0: O is what the
+    light ones leave, 2^-6 of their value.  An fp16 weight is off by half its smallest
+    step, 2^-25, of a reference 2^7 below the heaviest: n 2^-32 |v| in all.  A lane's sum
+    rounds once a tile of a warp (64 keys of every 256): n / 256 additions, 2^-24 each.
+    The rest as in the module's other test, a weight rounded once being off by 2^-11, and
+    y = 26 for every row."""
+    n, c0, vs = 1 << 20, 100, 2.0 ** -7
+    cache = skv.kv8_cache(1, 1, n, D, 128)
+    cache.k.zero_()
+    cache.k[:, :, 0] = c0
+    cache.v.fill_(100)
+    cache.v[:, :, 0] = 0
+    cache.k_scale.fill_(1.0)
+    cache.v_scale.fill_(vs)
+    scale = float(np.float32(26 * np.log(2.0) / (D * c0)))
+    q = torch.ones(1, rows, 1, D, dtype=DT[dtype], device="cuda")
+    out, lse = skv.attn_splitkv_decode_kv8(q, cache, scale, num_ctas=1)
+    heavy = 2.0 ** (scale * np.log2(np.e) * D * c0)
+    want, l_want = 100 * vs * (n - 1) / (n - 1 + heavy), np.log2(n - 1 + heavy)
+    sums = n / 256 * 2.0 ** -24
+    l_tol = 2.0 ** -18 * 26 + 2.0 ** -17 + 1.5 * sums
+    assert np.abs(O.to_f64(lse) - l_want).max() <= l_tol
+    tol = half_step(np.float64(want), dtype) + (2.0 ** -11 + 2 * np.log(2.0) * l_tol + 2.0 ** -16) * want + n * 2.0 ** -32 * 100 * vs
+    assert tol < want / 30
+    assert np.abs(O.to_f64(out) - want).max() <= tol
