@@ -470,7 +470,7 @@ skv_status kv8_fetch(const void* k_codes, const void* v_codes, const float* k_sc
  * O, LSE, kv_len and causal (as attn_splitkv_decode_causal) are those of
  * attn_splitkv_decode with K = codes * scale and V = codes * scale; the products
  * take the codes exactly.  A non-finite scale makes the rows that see its block
- * NaN.  num_ctas: the keys of all sequences and heads are divided evenly among
+ * NaN, whatever its codes (a scale of V: O, one of K: LSE and weights too).  num_ctas: the keys of all sequences and heads are divided evenly among
  * this many CTAs, 1..1024 (0 = automatic, attn_splitkv_kv8_plan with the device's
  * SM count); the division follows kv_len on the device.
  * weights: device fp32 [B, Hkv, capacity] (16-byte aligned) or NULL.  If given,

@@ -566,7 +566,9 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
     bool ok = true;
     for (int key0 = first; key0 < s1; key0 += kStride) {
       if (chunk_tile == 0) {
-        ks_chunk = ks_ahead;
+        // (an infinite scale becomes NaN: times a negative sum of codes it would be a
+        // logit of -inf, a key without weight)
+        ks_chunk = fmaf(ks_ahead, 0.f, ks_ahead);
         lv_chunk = __log2f(vs_ahead);  // -inf for a block of zeros
         fetch_scales(key0 + kChunk * kStride);
       }
