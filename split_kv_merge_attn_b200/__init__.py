@@ -6,7 +6,9 @@ the 8-bit cache: through a small extension module, whose checks take less time
 than their kernels), and every step of the computation runs in the library's
 sm_100a kernels.  PyTorch supplies device
 memory (outputs and workspace are allocated with ``torch.empty`` when the
-caller does not pass them) and streams.  There is no fallback: if the shared
+caller does not pass them) and streams; a call around the 8-bit cache that is
+given a stream of its own allocates there, and the tensors passed to it may be
+let go of before it has run.  There is no fallback: if the shared
 library is missing or a call fails, an exception is raised.
 
 Entry points (same names as the C ABI):

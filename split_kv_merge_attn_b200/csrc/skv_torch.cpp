@@ -14,6 +14,7 @@
 #include <ATen/ATen.h>
 #include <ATen/cuda/CUDAContext.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -138,28 +139,51 @@ bool truth(PyObject* o) {
 // Makes the tensors' device current for a call, and the caller's stream (its
 // address as an integer; None: the device's current one): what the call allocates
 // then belongs to the stream it runs on.  Memory of another stream could still be in
-// use there, and would be handed out again there before this call has run.
+// use there, and would be handed out again there before this call has run; so what the
+// caller passes is recorded as in use on the given stream, and what it gets as in use
+// on the current one.
 class On {
  public:
-  On(int dev, PyObject* stream) : device_(static_cast<c10::DeviceIndex>(dev)) {
+  On(int dev, PyObject* const* args, Py_ssize_t n) : device_(static_cast<c10::DeviceIndex>(dev)) {
+    const c10::cuda::CUDAStream now = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev));
+    cudaStream_t used = now.stream();
+    PyObject* stream = args[n - 1];  // the last argument of every call
     if (stream != Py_None) {
       void* p = PyLong_AsVoidPtr(stream);
       if (p == nullptr && PyErr_Occurred()) throw PythonError();
-      stream_.emplace(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(p), static_cast<c10::DeviceIndex>(dev)));
+      used = static_cast<cudaStream_t>(p);
+      if (used != now.stream()) {
+        caller_ = now;
+        stream_.emplace(c10::cuda::getStreamFromExternal(used, static_cast<c10::DeviceIndex>(dev)));
+        for (Py_ssize_t i = 0; i < n; ++i) record(args[i]);
+      }
     }
-    handle = reinterpret_cast<skv_stream_t>(c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream());
+    handle = reinterpret_cast<skv_stream_t>(used);
+  }
+  // a new output (not through the operator dispatch of at::empty)
+  at::Tensor empty(at::IntArrayRef shape, at::ScalarType dt) const {
+    at::Tensor t = scratch(shape, dt);
+    if (caller_) c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), *caller_);
+    return t;
+  }
+  // memory that the call alone uses
+  at::Tensor scratch(at::IntArrayRef shape, at::ScalarType dt) const {
+    return at::Tensor(at::detail::empty_cuda(shape, dt, device_.current_device(), std::nullopt));
   }
   skv_stream_t handle;
 
  private:
+  void record(PyObject* o) const {
+    if (PyTuple_Check(o)) {  // a cache
+      for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(o); ++i) record(PyTuple_GET_ITEM(o, i));
+    } else if (THPVariable_Check(o)) {
+      c10::cuda::CUDACachingAllocator::recordStream(THPVariable_Unpack(o).storage().data_ptr(), stream_->current_stream());
+    }
+  }
   c10::cuda::CUDAGuard device_;
+  std::optional<c10::cuda::CUDAStream> caller_;  // the current stream, where it is not the call's
   std::optional<c10::cuda::CUDAStreamGuard> stream_;
 };
-
-// (not through the operator dispatch of at::empty)
-at::Tensor empty(at::IntArrayRef shape, at::ScalarType dt, int dev) {
-  return at::Tensor(at::detail::empty_cuda(shape, dt, at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(dev)), std::nullopt));
-}
 
 // ------------------------------------------------------------ the cache
 
@@ -279,16 +303,16 @@ PyObject* py_rope_apply(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor& f = tensor(a[3], "inv_freq");
     const int64_t nf[1] = {f.numel()};
     const auto* pf = static_cast<const double*>(address(f, "inv_freq", nf, at::kDouble, dev));
-    const On on(dev, a[10]);
+    const On on(dev, a, n);
     at::Tensor qo, ko;
     void* pqo = opt(a[8], "q_out", q.sizes(), dt, dev);
     void* pko = opt(a[9], "k_out", k_shape, dt, dev);
     if (pqo == nullptr && a[8] == Py_None) {
-      qo = empty(q.sizes(), dt, dev);
+      qo = on.empty(q.sizes(), dt);
       pqo = qo.data_ptr();
     }
     if (a[1] != Py_None && a[9] == Py_None) {
-      ko = empty(k_shape, dt, dev);
+      ko = on.empty(k_shape, dt);
       pko = ko.data_ptr();
     }
     if (B * S > 0) {
@@ -329,7 +353,7 @@ PyObject* py_kv8_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const auto* pn = static_cast<const int32_t*>(opt(a[4], "num_new", b, at::kInt, dev));
     const auto* pc = static_cast<const int32_t*>(opt(a[6], "cu_seqlens", b1, at::kInt, dev));
     const skv_dtype code = half(dt, "k");
-    const On on(dev, a[8]);
+    const On on(dev, a, n);
     if (S != 0 && (T != 0 || layout != SKV_TND)) {
       check(g_lib.kv8_append(pk, pv, c.k, c.v, c.ks, c.vs, ps, pn, pc, static_cast<int>(c.B), static_cast<int>(c.Hkv),
                              small(S, "S"), small(T, "tokens"), static_cast<int>(c.capacity), static_cast<int>(c.D), c.block,
@@ -362,16 +386,16 @@ PyObject* py_kv8_fetch(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t b[1] = {c.B};
     const auto* ps = static_cast<const int32_t*>(opt(a[3], "start", b, at::kInt, dev));
     const auto* pl = static_cast<const int32_t*>(opt(a[4], "kv_len", b, at::kInt, dev));
-    const On on(dev, a[8]);
+    const On on(dev, a, n);
     at::Tensor ko, vo;
     void* pk = opt(a[6], "k_out", shape, dt, dev);
     void* pv = opt(a[7], "v_out", shape, dt, dev);
     if (a[6] == Py_None) {
-      ko = empty(shape, dt, dev);
+      ko = on.empty(shape, dt);
       pk = ko.data_ptr();
     }
     if (a[7] == Py_None) {
-      vo = empty(shape, dt, dev);
+      vo = on.empty(shape, dt);
       pv = vo.data_ptr();
     }
     if (rows != 0) {
@@ -405,17 +429,17 @@ PyObject* py_decode_kv8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     check(g_lib.plan(iB, iHq, iHkv, iLq, iN, iD, at::cuda::getDeviceProperties(static_cast<c10::DeviceIndex>(dev))->multiProcessorCount,
                      ctas, &ctas),
           "attn_splitkv_decode_kv8");
-    const On on(dev, a[11]);
+    const On on(dev, a, n);
     at::Tensor out, lse, ws;
     void* po = opt(a[7], "out", shape, dt, dev);
     if (a[7] == Py_None) {
-      out = empty(shape, dt, dev);
+      out = on.empty(shape, dt);
       po = out.data_ptr();
     }
     const bool want_lse = truth(a[9]);
     auto* pl = want_lse ? static_cast<float*>(opt(a[8], "lse", at::IntArrayRef(shape, 3), at::kFloat, dev)) : nullptr;
     if (want_lse && a[8] == Py_None) {
-      lse = empty(at::IntArrayRef(shape, 3), at::kFloat, dev);
+      lse = on.empty(at::IntArrayRef(shape, 3), at::kFloat);
       pl = static_cast<float*>(lse.data_ptr());
     }
     void* pws = nullptr;
@@ -429,7 +453,7 @@ PyObject* py_decode_kv8(PyObject*, PyObject* const* a, Py_ssize_t n) {
       bytes = g_lib.workspace(iB, iHq, iHkv, iLq, iN, iD, ctas, pw != nullptr);
       if (bytes > 0) {
         const int64_t size[1] = {static_cast<int64_t>(bytes)};
-        ws = empty(size, at::kByte, dev);
+        ws = on.scratch(size, at::kByte);
         pws = ws.data_ptr();
       }
     }
@@ -457,16 +481,16 @@ PyObject* py_kv8_evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const auto* pw = static_cast<const float*>(arg(a[2], "weights", from, at::kFloat, dev));
     auto* pt = static_cast<float*>(arg(a[3], "to_weights", to, at::kFloat, dev));
     const auto* pn = static_cast<const int32_t*>(opt(a[4], "kv_len", b, at::kInt, dev));
-    const On on(dev, a[10]);
+    const On on(dev, a, n);
     at::Tensor kept, len;
     auto* pk = static_cast<int32_t*>(opt(a[8], "kept", bhk, at::kInt, dev));
     auto* pl = static_cast<int32_t*>(opt(a[9], "new_len", b, at::kInt, dev));
     if (a[8] == Py_None) {
-      kept = empty(bhk, at::kInt, dev);
+      kept = on.empty(bhk, at::kInt);
       pk = static_cast<int32_t*>(kept.data_ptr());
     }
     if (a[9] == Py_None) {
-      len = empty(b, at::kInt, dev);
+      len = on.empty(b, at::kInt);
       pl = static_cast<int32_t*>(len.data_ptr());
     }
     check(g_lib.evict(c.k, c.v, c.ks, c.vs, pw, pn, t.k, t.v, t.ks, t.vs, pt, pk, pl, static_cast<int>(c.B),
