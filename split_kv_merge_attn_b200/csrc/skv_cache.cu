@@ -320,6 +320,10 @@ skv_status rope_apply(const void* q, const void* k, void* q_out, void* k_out, co
   if ((q_out != q && overlap(q_out, nq, q, nq)) || (k != nullptr && k_out != k && overlap(k_out, nk, k, nk)) ||
       overlap(q_out, nq, k, nk) || overlap(q, nq, k_out, nk) || overlap(q_out, nq, k_out, nk))
     return SKV_ERR_INVALID_ARG;
+  // every CTA reads positions and frequencies while others already write
+  const Span angles[] = {{positions, static_cast<size_t>(B) * S * 4}, {inv_freq, static_cast<size_t>(rotary_dim) * 4}};
+  for (const Span& x : angles)
+    if (overlap(q_out, nq, x.p, x.n) || overlap(k_out, nk, x.p, x.n)) return SKV_ERR_INVALID_ARG;
   if (S == 0) return SKV_OK;
   RopeArgs a;
   a.x[0] = q;
