@@ -413,7 +413,9 @@ skv_status rope_apply(const void* q, const void* k, void* q_out, void* k_out, co
  *   NTK     base -> base * factor^(rotary_dim / (rotary_dim - 2))
  *   YARN    f (1 - g) + f / factor g with g rising from 0 to 1 between the
  *           pairs that turn beta_fast and beta_slow times over original_len
- *           positions (Peng et al., "YaRN", 2023); factor 0.1 ln(factor) + 1.
+ *           positions (Peng et al., "YaRN", 2023), rounded outwards to whole
+ *           pairs and held to [0, rotary_dim - 1], where the second may lie
+ *           behind the last pair; factor 0.1 ln(factor) + 1.
  * factor >= 1 (ignored for NONE); original_len, beta_* are read for YARN only. */
 typedef enum { SKV_ROPE_NONE = 0, SKV_ROPE_LINEAR = 1, SKV_ROPE_NTK = 2, SKV_ROPE_YARN = 3 } skv_rope_scaling;
 skv_status rope_inv_freq(int rotary_dim, double base, skv_rope_scaling scaling, double factor, int original_len,

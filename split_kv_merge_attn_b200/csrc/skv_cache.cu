@@ -284,7 +284,8 @@ skv_status rope_inv_freq(int rotary_dim, double base, skv_rope_scaling scaling, 
       return rotary_dim * std::log(original_len / (turns * 2.0 * 3.141592653589793)) / (2.0 * std::log(base));
     };
     lo = std::max(std::floor(pair_of(beta_fast)), 0.0);
-    hi = std::min(std::ceil(pair_of(beta_slow)), half - 1.0);
+    // (may lie behind the last pair: all of them then turn more than beta_slow times)
+    hi = std::min(std::ceil(pair_of(beta_slow)), rotary_dim - 1.0);
   }
   for (int i = 0; i < half; ++i) {
     double f = std::pow(base, -2.0 * i / rotary_dim);
