@@ -447,7 +447,7 @@ typedef enum { SKV_INT8 = 0, SKV_E4M3 = 1 } skv_code;
  * block's scale non-finite and its codes 0, so that all of it reads as NaN.
  *
  * k_new, v_new: [B, Hkv, S, D] / [B, S, Hkv, D], or TND [T, Hkv, D] with
- * cu_seqlens [B + 1] and S = the longest sequence.  num_new: device int32 [B]
+ * cu_seqlens [B + 1] and S >= the longest sequence, S <= T.  num_new: device int32 [B]
  * or NULL (= S), dense layouts only: the first num_new[b] tokens of b are
  * appended.  start, num_new and lengths are read on the device and clamped
  * (start to [0, capacity], counts to [0, S]); tokens that do not fit the

@@ -639,7 +639,7 @@ def kv8_append(cache: KV8Cache, k, v, start, num_new=None, layout: str = "HND", 
     """Quantises new tokens into the cache, in place.
 
     k, v: [B,Hkv,S,D] (HND), [B,S,Hkv,D] (NHD), or [T,Hkv,D] (TND, with int32
-    cu_seqlens [B+1] and max_seqlen).  Token i of sequence b goes to position
+    cu_seqlens [B+1] and max_seqlen, any bound of the sequences' lengths).  Token i of sequence b goes to position
     start[b] + i (int32 device tensor [B]); num_new: optional int32 [B], the
     first num_new[b] tokens only (dense layouts).  Positions and counts are
     clamped on the device; tokens behind the capacity are dropped.  A block's

@@ -21,6 +21,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -338,7 +339,7 @@ PyObject* py_kv8_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (a[6] == Py_None || a[7] == Py_None || a[4] != Py_None || k.dim() != 3)
         refuse("TND rows are [tokens, heads, D], with cu_seqlens and max_seqlen and without num_new");
       T = k.size(0);
-      S = integer(a[7], "max_seqlen");
+      S = std::min<int64_t>(integer(a[7], "max_seqlen"), T);  // no sequence is longer than all rows
       shape = {T, c.Hkv, c.D};
     } else {
       if (a[6] != Py_None || a[7] != Py_None || k.dim() != 4)
