@@ -113,8 +113,11 @@ uint64_t skv_launch_count(void) { return skv::launch_count(); }
 skv_status skv_device_error(int* code) {
   if (code == nullptr) return SKV_ERR_INVALID_ARG;
   int first = 0, second = 0;
-  int e = skv::read_and_clear_device_error(&first);
-  if (e == 0) e = skv::read_and_clear_cache_error(&second);
+  // both words are read before either is cleared: a read that fails loses nothing
+  int e = skv::read_device_error(&first);
+  if (e == 0) e = skv::read_cache_error(&second);
+  if (e == 0 && first != 0) e = skv::clear_device_error();
+  if (e == 0 && second != 0) e = skv::clear_cache_error();
   if (e != 0) return cuda_status(e);
   *code = first != 0 ? first : second;
   return SKV_OK;

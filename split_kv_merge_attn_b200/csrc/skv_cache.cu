@@ -23,15 +23,11 @@
 
 namespace skv {
 
-int read_and_clear_cache_error(int* code) {
-  int v = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(&v, g_skv_device_error, sizeof(int));
-  if (e != cudaSuccess) return e;
+int read_cache_error(int* code) { return cudaMemcpyFromSymbol(code, g_skv_device_error, sizeof(int)); }
+
+int clear_cache_error() {
   const int zero = 0;
-  e = cudaMemcpyToSymbol(g_skv_device_error, &zero, sizeof(int));
-  if (e != cudaSuccess) return e;
-  *code = v;
-  return 0;
+  return cudaMemcpyToSymbol(g_skv_device_error, &zero, sizeof(int));
 }
 
 namespace {

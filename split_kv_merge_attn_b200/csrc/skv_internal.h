@@ -113,10 +113,13 @@ int launch_smooth_k(const void* k, void* k_smoothed, float* kmean, float* partia
                     int Hkv, int Sk, int max_len, int D, skv_dtype dt, skv_layout layout, skv_stream_t stream,
                     int kv_ranges = 1, const int32_t* kv_bounds = nullptr);
 
-int read_and_clear_device_error(int* code);
+// The device error word (read: after the device's work so far).
+int read_device_error(int* code);
+int clear_device_error();
 // The same for the error word of the 8-bit cache's kernels (a translation unit
 // of their own, and so a word of their own).
-int read_and_clear_cache_error(int* code);
+int read_cache_error(int* code);
+int clear_cache_error();
 
 // Elementwise evaluation of the prefill's FMA-pipe exp2 (diagnostics).
 int launch_exp2_fma(const float* x, float* y, int64_t n, skv_stream_t stream);

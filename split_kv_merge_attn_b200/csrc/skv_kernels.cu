@@ -21,17 +21,14 @@
 
 namespace skv {
 
-int read_and_clear_device_error(int* code) {
-  cudaError_t e = cudaDeviceSynchronize();
-  if (e != cudaSuccess) return e;
-  int v = 0;
-  e = cudaMemcpyFromSymbol(&v, g_skv_device_error, sizeof(int));
-  if (e != cudaSuccess) return e;
+int read_device_error(int* code) {
+  const cudaError_t e = cudaDeviceSynchronize();
+  return e != cudaSuccess ? e : cudaMemcpyFromSymbol(code, g_skv_device_error, sizeof(int));
+}
+
+int clear_device_error() {
   const int zero = 0;
-  e = cudaMemcpyToSymbol(g_skv_device_error, &zero, sizeof(int));
-  if (e != cudaSuccess) return e;
-  *code = v;
-  return 0;
+  return cudaMemcpyToSymbol(g_skv_device_error, &zero, sizeof(int));
 }
 
 namespace {
