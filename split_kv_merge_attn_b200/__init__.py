@@ -34,7 +34,6 @@ from typing import NamedTuple, Optional, Sequence, Tuple
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libsplitkv.so")
-TORCH_LIB_PATH = os.path.join(HERE, "_skv_torch.so")
 
 SKV_OK, SKV_ERR_INVALID_ARG, SKV_ERR_UNSUPPORTED, SKV_ERR_WORKSPACE_TOO_SMALL, SKV_ERR_CUDA = range(5)
 DTYPES = {"bf16": 0, "fp16": 1, "fp32": 2}
@@ -207,9 +206,11 @@ _TORCH_FUNCTIONS = ("rope_apply", "kv8_append", "kv8_fetch", "attn_splitkv_kv8_p
 def _torch_calls():
     """The extension module that marshals the short calls (csrc/skv_torch.cpp), loaded on first use."""
     _torch()
-    if not os.path.exists(TORCH_LIB_PATH):
-        raise RuntimeError(f"{TORCH_LIB_PATH} is missing: build it with `python -m split_kv_merge_attn_b200._build`")
-    spec = importlib.util.spec_from_file_location("split_kv_merge_attn_b200._skv_torch", TORCH_LIB_PATH)
+    from . import _build
+    path = _build.torch_lib()
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is missing: build it with `python -m split_kv_merge_attn_b200._build`")
+    spec = importlib.util.spec_from_file_location("split_kv_merge_attn_b200._skv_torch", path)
     m = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(m)
     m.bind(SkvError, *(ctypes.cast(getattr(lib(), f), ctypes.c_void_p).value for f in _TORCH_FUNCTIONS))

@@ -1,23 +1,27 @@
 """Builds the in-tree shared library ``libsplitkv.so`` for sm_100a with nvcc, and
-``_skv_torch.so``, the extension module that marshals PyTorch tensors for the
-short calls, with the host compiler.
+``_skv_torch.<PyTorch>.<Python>.so``, the extension module that marshals PyTorch
+tensors for the short calls, with the host compiler.  The module is made of
+PyTorch's C++ classes, so it belongs to one version of PyTorch and of Python, which its
+name holds: after a change of either it is built anew.  Without PyTorch
+only the library is built.
 
 Usage: ``python -m split_kv_merge_attn_b200._build`` (or ``build()``).  Both are
 written next to this file so they travel with the source tree.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libsplitkv.so")
-TORCH_LIB = os.path.join(HERE, "_skv_torch.so")
 
 SOURCES = ["skv_kernels.cu", "skv_abi.cpp", "skv_noalloc.cu", "skv_cache.cu"]
 HEADERS = ["skv_device.cuh", "skv_internal.h", "merge_state.cuh", "decode.cuh", "prefill.cuh",
@@ -42,9 +46,14 @@ def command(out: str = LIB, extra=None):
     return cmd
 
 
-def torch_command(out: str = TORCH_LIB):
-    import sysconfig
+def torch_lib() -> str:
+    """Path of the extension module for the PyTorch and Python that run."""
+    import torch
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    return os.path.join(HERE, f"_skv_torch.torch-{torch.__version__}-abi{abi}{sysconfig.get_config_var('EXT_SUFFIX')}")
 
+
+def torch_command(out: str):
     import torch
     from torch.utils import cpp_extension
     root = os.path.dirname(torch.__file__)
@@ -79,8 +88,11 @@ def _run(cmd, name: str, verbose: bool) -> None:
 def build(force: bool = False, verbose: bool = False, extra=None) -> str:
     if force or _stale(LIB, SOURCES + HEADERS):
         _run(command(extra=extra), "libsplitkv.so", verbose)
-    if force or _stale(TORCH_LIB, ["skv_torch.cpp"]):
-        _run(torch_command(), "_skv_torch.so", verbose)
+    if importlib.util.find_spec("torch") is None:
+        if verbose:
+            print("PyTorch is not installed: only the C library is built")
+    elif force or _stale(torch_lib(), ["skv_torch.cpp"]):
+        _run(torch_command(torch_lib()), os.path.basename(torch_lib()), verbose)
     return LIB
 
 
