@@ -605,10 +605,47 @@ def rope_apply(q, k, positions, inv_freq, layout: str = "HND", interleaved: bool
     positions: int32 [B,S] (TND: [T]); inv_freq: float64 [R/2], R <= D dimensions
     turn (D and R multiples of 16), the others are copied.  interleaved: pairs
     (2i, 2i+1) instead of (i, i + R/2).  inverse: the transpose, i.e. the
-    gradient of the inputs given that of the outputs.  q_out=q, k_out=k work in
+    gradient of the inputs given that of the outputs; autograd takes it where q or k
+    requires a gradient (q_out, k_out are refused then).  q_out=q, k_out=k work in
     place.  Returns (q_out, k_out)."""
-    return _torch_calls().rope_apply(q, k, positions, inv_freq, _layout(layout), interleaved, factor, inverse, q_out, k_out,
-                                     _handle(stream))
+    how = (_layout(layout), interleaved, factor, inverse)
+    out = _torch_calls().rope_apply(q, k, positions, inv_freq, *how, q_out, k_out, _handle(stream))
+    if out is None:  # autograd has to record it
+        _expect(q_out is None and k_out is None, "q_out and k_out cannot be given where autograd records the call")
+        _expect(not inv_freq.requires_grad, "rope_apply has no gradient of inv_freq")
+        out = _rope_function().apply(q, k, positions, inv_freq, *how, _handle(stream))
+    return out
+
+
+@functools.lru_cache(maxsize=None)
+def _rope_function():
+    """rope_apply as a differentiable function; its gradient is the transpose, on
+    the stream that autograd makes current."""
+    torch = _torch()
+
+    class Rope(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, q, k, positions, inv_freq, layout, interleaved, factor, inverse, stream):
+            ctx.save_for_backward(positions, inv_freq)
+            ctx.how = (layout, interleaved, factor, not inverse)
+            ctx.set_materialize_grads(False)
+            out = _torch_calls().rope_apply(q, k, positions, inv_freq, layout, interleaved, factor, inverse, None, None,
+                                            stream)
+            ctx.mark_non_differentiable(*(o for o, x in zip(out, (q, k)) if x is not None and not x.requires_grad))
+            return out
+
+        @staticmethod
+        def backward(ctx, *grads):
+            at = [i for i, g in enumerate(grads) if g is not None and ctx.needs_input_grad[i]]
+            got = [None, None]
+            if at:
+                ready = [g if g.data_ptr() % 16 == 0 else g.clone() for g in (grads[i].contiguous() for i in at)]
+                out = Rope.apply(*ready, *[None] * (2 - len(at)), *ctx.saved_tensors, *ctx.how, None)
+                for i, g in zip(at, out):
+                    got[i] = g
+            return (*got, *[None] * 7)
+
+    return Rope
 
 
 # ------------------------------------------------------------------ 8-bit cache

@@ -12,6 +12,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/cuda/CUDAContext.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDACachingAllocator.h>
@@ -266,9 +267,24 @@ PyObject* result(PyObject* given, const at::Tensor& made) {
   return THPVariable_Wrap(made);
 }
 
+// Whether autograd would record an operation on this argument.
+bool differentiated(PyObject* o) {
+  return THPVariable_Check(o) && THPVariable_Unpack(o).requires_grad() && at::GradMode::is_enabled();
+}
+
+// Tells autograd that a tensor of the caller's was written.
+void written(PyObject* o) {
+  if (o == Py_None) return;
+  const at::Tensor& t = THPVariable_Unpack(o);
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // rope_apply(q, k, positions, inv_freq, layout, interleaved, factor, inverse, q_out, k_out, stream)
+// None, and nothing done, where autograd has to record it.
 PyObject* py_rope_apply(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 11, [&]() -> PyObject* {
+    for (const int i : {0, 1, 3, 8, 9})
+      if (differentiated(a[i])) return Py_NewRef(Py_None);
     const at::Tensor& q = tensor(a[0], "q");
     const int layout = integer(a[4], "layout");
     if (q.dim() != (layout == SKV_TND ? 3 : 4)) refuse("q has " + std::to_string(q.dim()) + " dimensions, not the layout's");
@@ -321,6 +337,8 @@ PyObject* py_rope_apply(PyObject*, PyObject* const* a, Py_ssize_t n) {
                              small(D, "D"), small(2 * nf[0], "inv_freq"), static_cast<float>(real(a[6])), code,
                              static_cast<skv_layout>(layout), truth(a[5]), truth(a[7]), on.handle),
             "rope_apply");
+      written(a[8]);
+      written(a[9]);
     }
     return pair(result(a[8], qo), result(a[9], ko));
   });
