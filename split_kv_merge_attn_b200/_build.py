@@ -38,7 +38,7 @@ def nvcc() -> str:
 
 def command(out: str = LIB, extra=None):
     cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-shared",
-           "-cudart", "static", "-I", INCLUDE, "-I", CSRC]
+           "-cudart", "static", "-t", "0", "-I", INCLUDE, "-I", CSRC]  # -t 0: the sources at the same time
     cmd += [os.path.join(CSRC, s) for s in SOURCES]
     cmd += ["-o", out]
     if extra:
