@@ -170,6 +170,13 @@ __device__ __forceinline__ void codes_to_half_even_odd(uint32_t w, uint32_t& h0,
   }
 }
 
+// Two fp16 numbers, the largest finite ones where a value lies above them (NaN stays).
+__device__ __forceinline__ uint32_t pack_f16x2_finite(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 // The weights of a tile from its scores s (x = s f): p = 2^(x - m), added to the
 // sums, and fp16 p vs / 2^mv, the A fragments of P V.  kSplit: what that rounding
 // leaves, in fp16 too (pl); kLow: the same in rows 8-15, which hold no rows of their
@@ -205,10 +212,12 @@ __device__ __forceinline__ void tile_weights(const float (&s)[2 * kGroups][4], c
           pw.x = sa == -INFINITY ? 0.f : pw.x;
           pw.y = sb == -INFINITY ? 0.f : pw.y;
         }
-        pa[gr][2 * i + hr] = pack_f16x2(pw.x, pw.y);
+        // (logits beyond 2^24 are whole numbers or coarser in fp32: a weight may then lie
+        // above 2^15 by the exponents' error, and must not become infinite)
+        pa[gr][2 * i + hr] = pack_f16x2_finite(pw.x, pw.y);
         if constexpr (kSplit || kLow) {
           const float2 kept = unpack2<__half>(pa[gr][2 * i + hr]);
-          (kLow ? pa[gr][2 * i + 1] : pl[gr][2 * i + hr]) = pack_f16x2(pw.x - kept.x, pw.y - kept.y);
+          (kLow ? pa[gr][2 * i + 1] : pl[gr][2 * i + hr]) = pack_f16x2_finite(pw.x - kept.x, pw.y - kept.y);
         } else if constexpr (kHalves == 1) {
           pa[gr][2 * i + 1] = 0u;
         }

@@ -74,3 +74,32 @@ def test_many_light_keys_beside_a_heavy_one(D, rows, dtype):
     tol = half_step(np.float64(want), dtype) + (2.0 ** -11 + 2 * np.log(2.0) * l_tol + 2.0 ** -16) * want + n * 2.0 ** -32 * 100 * vs
     assert tol < want / 30
     assert np.abs(O.to_f64(out) - want).max() <= tol
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("rows", [1, 16])
+@pytest.mark.parametrize("power,unit", [(12, 1), (14, 1), (15, 1), (17, 1), (17, 2), (17, 4)])
+def test_logits_of_millions_stay_finite(power, unit, rows, dtype):
+    """Logits near 100 unit 2^power, where fp32 holds them to quarters at best and to
+    whole steps of 4 at worst, and the exponents of the weights are off by as much as
+    that: weights a few such steps above fp16's largest value must not become infinite.
+    O is a value of V times what the exponents are off by, at most 2^6 either way; the
+    LSE is right to 2^-20 of itself (the fp32 product of scale, K's scale and the sum),
+    plus log2 n and a step."""
+    n = 2048
+    for step in range(1, 10):
+        for frac in (0.0, 0.3, 0.5, 0.8):
+            cache = skv.kv8_cache(1, 1, n, 64, 16)
+            cache.k.zero_()
+            cache.k[..., 0] = 100
+            cache.k[0, 0, :, 1] = (torch.arange(n, device="cuda") // 256 * step).clamp(max=100).to(torch.int8)
+            cache.v.fill_(100)
+            cache.k_scale.fill_(1.0)
+            cache.v_scale.fill_(2.0 ** (frac - 7))
+            q = torch.zeros(1, rows, 1, 64, dtype=DT[dtype], device="cuda")
+            q[..., 0], q[..., 1] = 2.0 ** (power - 2), 0.25  # (fp16 ends below 2^16)
+            out, lse = skv.attn_splitkv_decode_kv8(q, cache, float(4 * unit * np.log(2.0)), num_ctas=1)
+            want = 100 * 2.0 ** (frac - 7)
+            assert torch.isfinite(out).all() and (out.float() <= 64 * want).all() and (out.float() >= want / 64).all(), (step, frac)
+            x = unit * (100.0 * 2 ** power + 7 * step)
+            assert ((lse.double() - x).abs() <= 2.0 ** -20 * x + 11 + 4).all()
