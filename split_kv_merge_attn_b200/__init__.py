@@ -608,12 +608,13 @@ def rope_apply(q, k, positions, inv_freq, layout: str = "HND", interleaved: bool
     gradient of the inputs given that of the outputs; autograd takes it where q or k
     requires a gradient (q_out, k_out are refused then).  q_out=q, k_out=k work in
     place.  Returns (q_out, k_out)."""
-    how = (_layout(layout), interleaved, factor, inverse)
-    out = _torch_calls().rope_apply(q, k, positions, inv_freq, *how, q_out, k_out, _handle(stream))
+    out = _torch_calls().rope_apply(q, k, positions, inv_freq, _layout(layout), interleaved, factor, inverse, q_out, k_out,
+                                    _handle(stream))
     if out is None:  # autograd has to record it
         _expect(q_out is None and k_out is None, "q_out and k_out cannot be given where autograd records the call")
         _expect(not inv_freq.requires_grad, "rope_apply has no gradient of inv_freq")
-        out = _rope_function().apply(q, k, positions, inv_freq, *how, _handle(stream))
+        out = _rope_function().apply(q, k, positions, inv_freq, _layout(layout), interleaved, factor, inverse,
+                                     _handle(stream))
     return out
 
 
