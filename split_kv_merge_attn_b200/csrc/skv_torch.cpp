@@ -146,21 +146,20 @@ bool truth(PyObject* o) {
 // on the current one.
 class On {
  public:
-  On(int dev, PyObject* const* args, Py_ssize_t n) : device_(static_cast<c10::DeviceIndex>(dev)) {
-    const c10::cuda::CUDAStream now = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev));
-    cudaStream_t used = now.stream();
+  On(int dev, PyObject* const* args, Py_ssize_t n) : dev_(static_cast<c10::DeviceIndex>(dev)), device_(dev_) {
+    const c10::cuda::CUDAStream now = c10::cuda::getCurrentCUDAStream(dev_);
+    handle = reinterpret_cast<skv_stream_t>(now.stream());
     PyObject* stream = args[n - 1];  // the last argument of every call
     if (stream != Py_None) {
       void* p = PyLong_AsVoidPtr(stream);
       if (p == nullptr && PyErr_Occurred()) throw PythonError();
-      used = static_cast<cudaStream_t>(p);
-      if (used != now.stream()) {
+      if (p != now.stream()) {
         caller_ = now;
-        stream_.emplace(c10::cuda::getStreamFromExternal(used, static_cast<c10::DeviceIndex>(dev)));
+        stream_.emplace(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(p), dev_));
+        handle = reinterpret_cast<skv_stream_t>(static_cast<cudaStream_t>(p));
         for (Py_ssize_t i = 0; i < n; ++i) record(args[i]);
       }
     }
-    handle = reinterpret_cast<skv_stream_t>(used);
   }
   // a new output (not through the operator dispatch of at::empty)
   at::Tensor empty(at::IntArrayRef shape, at::ScalarType dt) const {
@@ -170,7 +169,7 @@ class On {
   }
   // memory that the call alone uses
   at::Tensor scratch(at::IntArrayRef shape, at::ScalarType dt) const {
-    return at::Tensor(at::detail::empty_cuda(shape, dt, device_.current_device(), std::nullopt));
+    return at::Tensor(at::detail::empty_cuda(shape, dt, at::Device(at::kCUDA, dev_), std::nullopt));
   }
   skv_stream_t handle;
 
@@ -182,6 +181,7 @@ class On {
       c10::cuda::CUDACachingAllocator::recordStream(THPVariable_Unpack(o).storage().data_ptr(), stream_->current_stream());
     }
   }
+  c10::DeviceIndex dev_;
   c10::cuda::CUDAGuard device_;
   std::optional<c10::cuda::CUDAStream> caller_;  // the current stream, where it is not the call's
   std::optional<c10::cuda::CUDAStreamGuard> stream_;
@@ -267,10 +267,7 @@ PyObject* result(PyObject* given, const at::Tensor& made) {
   return THPVariable_Wrap(made);
 }
 
-// Whether autograd would record an operation on this argument.
-bool differentiated(PyObject* o) {
-  return THPVariable_Check(o) && THPVariable_Unpack(o).requires_grad() && at::GradMode::is_enabled();
-}
+bool needs_gradient(PyObject* o) { return o != Py_None && THPVariable_Check(o) && THPVariable_Unpack(o).requires_grad(); }
 
 // Tells autograd that a tensor of the caller's was written.
 void written(PyObject* o) {
@@ -283,8 +280,9 @@ void written(PyObject* o) {
 // None, and nothing done, where autograd has to record it.
 PyObject* py_rope_apply(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 11, [&]() -> PyObject* {
-    for (const int i : {0, 1, 3, 8, 9})
-      if (differentiated(a[i])) return Py_NewRef(Py_None);
+    if (at::GradMode::is_enabled())
+      for (const int i : {0, 1, 3, 8, 9})
+        if (needs_gradient(a[i])) return Py_NewRef(Py_None);
     const at::Tensor& q = tensor(a[0], "q");
     const int layout = integer(a[4], "layout");
     if (q.dim() != (layout == SKV_TND ? 3 : 4)) refuse("q has " + std::to_string(q.dim()) + " dimensions, not the layout's");
