@@ -471,7 +471,12 @@ skv_status kv8_fetch(const void* k_codes, const void* v_codes, const float* k_sc
  *
  * O, LSE, kv_len and causal (as attn_splitkv_decode_causal) are those of
  * attn_splitkv_decode with K = codes * scale and V = codes * scale; the products
- * take the codes exactly.  A non-finite scale makes the rows that see its block
+ * take the codes exactly, with fp32 sums.  q enters them in fp16 relative to its
+ * row's largest value (what lies 2^-25 below that is lost), a softmax weight in fp16
+ * relative to about the row's largest: in two numbers, 2^-22 of itself, where a kv
+ * head has at most 8 query rows and for fp16 outputs, in one, 2^-11 at most, for bf16
+ * outputs of more rows; weights 2^-32 of the largest and less add nothing to O, only
+ * to LSE and the keys' weights.  A non-finite scale makes the rows that see its block
  * NaN, whatever its codes (a scale of V: O, one of K: LSE and weights too).  num_ctas: the keys of all sequences and heads are divided evenly among
  * this many CTAs, 1..1024 (0 = automatic, attn_splitkv_kv8_plan with the device's
  * SM count); the division follows kv_len on the device.

@@ -22,17 +22,21 @@
 // references follow the maxima loosely (within a factor of 2^8), and the weights'
 // lies 2^7 below: they end at 2^15, and what is dropped lies 2^-32 below the heaviest.
 //
-// What bounds it: bytes, and next the turning of codes into fp16.  At HBM rate an
-// SM receives about 23 codes per clock; turning them costs 1.25 (K) and 1.5 (V)
-// lane instructions each for int8, less for e4m3, about a quarter of the issue
-// slots, and the 16 rows' MMAs about as much again, so mma.sync nearly keeps pace
-// (tcgen05 would want 128 rows).  Whole calls, bf16 q, one row a head (a copy
-// reaches 6.6 TB/s):
-//   D = 64,  B = 16, 16 / 16 heads, 16384 keys: e4m3 87.0 us (6.2 TB/s), int8 100.4 (5.4)
-//   D = 128, B = 2, 32 / 8 heads, 32768 keys:   e4m3 27.3 us (4.9 TB/s), int8 30.8 (4.4)
-//   D = 256, B = 1, 16 / 4 heads, 131072 keys:  e4m3 50.6 us (5.3 TB/s), int8 57.7 (4.7)
-//   D = 128, B = 1, 32 / 8 heads, 4096 keys:    e4m3 8.5 us, int8 9.0: latency
-// Of these about 5 us are the start, the four warps' combine and the merge launch.
+// What bounds it: bytes at D = 64 and e4m3 (6.1 TB/s; a copy reaches 6.6), else the
+// latency of each warp's own chain of arrival, conversion, Q K^T, softmax and P V, with
+// the two warps a scheduler that registers allow.  At D = 128, int8, 32768 keys nothing
+// is saturated: issue 41%, tensor pipe 30%, DRAM 54%; of the 4.8 cycles between two
+// instructions of a warp 1.6 are fixed latencies of the instruction before, 0.8 waits
+// for loads and barriers, 0.4 for a busy pipe.  (Turning a code costs 1.25 (K) and 1.5
+// (V) lane instructions for int8, less for e4m3; tcgen05 would want 128 rows.)  Whole
+// calls, bf16 q, one row a head:
+//   D = 64,  B = 16, 16 / 16 heads, 16384 keys: e4m3 87.5 us (6.1 TB/s), int8 99.0 (5.4)
+//   D = 128, B = 2, 32 / 8 heads, 32768 keys:   e4m3 28.3 us (4.8 TB/s), int8 30.5 (4.4)
+//   D = 256, B = 1, 16 / 4 heads, 131072 keys:  e4m3 49.7 us (5.4 TB/s), int8 56.2 (4.8)
+//   D = 128, B = 1, 32 / 8 heads, 4096 keys:    e4m3 8.7 us, int8 8.9: latency
+// Of these about 5 us are the start, the four warps' combine and the merge launch: at
+// 4096 keys the decode over 16-bit keys, of fewer parts, takes 6.8 us (at 32768 keys,
+// B = 2, 45.3).
 //
 // Layout: the order of a product's summands is free as long as both operands
 // agree, so of a key row a thread takes the 32 contiguous codes at 32 (lane & 3)
@@ -230,7 +234,7 @@ __device__ __forceinline__ void tile_weights(const float (&s)[2 * kGroups][4], c
 
 // kHalves: 1 where a unit has at most 8 query rows (MMA rows 0-7), which leaves out
 // half the softmax, else 2 (with one row, bf16: B = 16, 16 heads, D = 64, 16384 keys, e4m3
-// 87.0 us against 95.5, int8 100.4 against 103.9; more rows need 2).
+// 87.5 us against 95.5, int8 99.0 against 103.9; more rows need 2).
 template <int D, typename T, bool kE4M3, bool kLogits, int kHalves>
 __global__ void __launch_bounds__(kKv8Threads, 2)
     decode_kv8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -526,7 +530,7 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
     // 64, 16384 keys, e4m3 87.5 us against 87.0, int8 99.0 against 100.7; D = 256, 131072
     // keys, e4m3 49.7 against 50.7).  Of 16 rows that takes twice the MMAs of P V (B = 2, 32 /
     // 8 heads, Lq = 4, D = 128, 32768 keys, int8: 37.5 us against 31.6): fp16 outputs have
-    // it, bf16 ones have one number, whose error is an eighth of their half step at most.
+    // it, bf16 ones have one number, off by an eighth of bf16's own 2^-8 at most.
     constexpr bool kLow = kHalves == 1;
     constexpr bool kSplit = std::is_same<T, __half>::value && kHalves == 2;
     constexpr int kNt = kTileKeys / 8;
