@@ -16,9 +16,10 @@
 // fp32 sums whatever the type of q: a q row is multiplied by a power of two
 // that brings its largest magnitude into [1, 2) (exact but for values 2^-14
 // times smaller), and ks, that power and log2(e) scale the fp32 logits.  For
-// P V the weights carry the block's scale: p_j vs_j is kept relative to its own
-// running maximum M >= x_j + log2 vs_j, apart from the softmax's m, so that the
-// fp16 weights use their range however much the scales of V differ.  Both
+// P V the weights carry the block's scale: p_j vs_j is kept relative to a reference
+// of its own, 2^d beside the softmax's 2^m with d >= x_j - m + log2 vs_j, so that the
+// fp16 weights use their range however much the scales of V differ (and d is small
+// whatever the logits: kept as m + d it lost V's scale beside large ones).  Both
 // references follow the maxima loosely (within a factor of 2^8), and the weights'
 // lies 2^7 below: they end at 2^15, and what is dropped lies 2^-32 below the heaviest.
 //
@@ -174,21 +175,16 @@ __device__ __forceinline__ void codes_to_half_even_odd(uint32_t w, uint32_t& h0,
   }
 }
 
-// Two fp16 numbers, the largest finite ones where a value lies above them (NaN stays).
-__device__ __forceinline__ uint32_t pack_f16x2_finite(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 // The weights of a tile from its scores s (x = s f): p = 2^(x - m), added to the
-// sums, and fp16 p vs / 2^mv, the A fragments of P V.  kSplit: what that rounding
+// sums, and fp16 p vs / 2^d, the A fragments of P V.  kSplit: what that rounding
 // leaves, in fp16 too (pl); kLow: the same in rows 8-15, which hold no rows of their
-// own (kHalves = 1).
-template <int kGroups, int kHalves, bool kMasked, bool kSplit, bool kLow>
+// own (kHalves = 1).  kCareful: some keys are masked (s = -inf), or m is so large that
+// x must be rounded as it was for m: fused with the difference, the product's own rounding,
+// 2^-24 of it, would be in p's exponent.
+template <int kGroups, int kHalves, bool kCareful, bool kSplit, bool kLow>
 __device__ __forceinline__ void tile_weights(const float (&s)[2 * kGroups][4], const float (&f)[kHalves][kGroups],
                                              const float (&lv)[kGroups], const float (&m)[kHalves],
-                                             const float (&mv)[kHalves], float (&lsum)[kHalves], uint32_t (&pa)[kGroups][4],
+                                             const float (&d)[kHalves], float (&lsum)[kHalves], uint32_t (&pa)[kGroups][4],
                                              uint32_t (&pl)[kSplit ? kGroups : 1][4]) {
 #pragma unroll
   for (int hr = 0; hr < kHalves; ++hr) {
@@ -196,32 +192,32 @@ __device__ __forceinline__ void tile_weights(const float (&s)[2 * kGroups][4], c
     const uint64_t minus_m = f2_pack(-m[hr], -m[hr]);
 #pragma unroll
     for (int gr = 0; gr < kGroups; ++gr) {
-      // p vs / 2^mv = p * 2^(m + log2 vs - mv), kept finite where m lies far above
-      // the keys that set mv: their p is 0 then, and 0 * inf is not
-      const float w = min_nan(ex2_approx(m[hr] + lv[gr] - mv[hr]), 3.0e38f);
+      // p vs / 2^d = p * 2^(log2 vs - d), kept finite where m lies far above the keys
+      // that set d: their p is 0 then, and 0 * inf is not
+      const float w = min_nan(ex2_approx(lv[gr] - d[hr]), 3.0e38f);
       const uint64_t ww = f2_pack(w, w), ff = f2_pack(f[hr][gr], f[hr][gr]);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const float sa = s[2 * gr + i][2 * hr], sb = s[2 * gr + i][2 * hr + 1];
-        const float2 x = f2_unpack(ffma2(f2_pack(sa, sb), ff, minus_m));
+        const float2 x = kCareful ? make_float2(__fsub_rn(__fmul_rn(sa, f[hr][gr]), m[hr]),
+                                                __fsub_rn(__fmul_rn(sb, f[hr][gr]), m[hr]))
+                                  : f2_unpack(ffma2(f2_pack(sa, sb), ff, minus_m));
         float2 p = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-        if constexpr (kMasked) {  // a masked key's weight is 0 whatever its scales
+        if constexpr (kCareful) {  // a masked key's weight is 0 whatever its scales
           p.x = sa == -INFINITY ? 0.f : p.x;
           p.y = sb == -INFINITY ? 0.f : p.y;
         }
         const uint64_t pp = f2_pack(p.x, p.y);
         sum = fadd2(sum, pp);
         float2 pw = f2_unpack(fmul2(pp, ww));
-        if constexpr (kMasked) {
+        if constexpr (kCareful) {
           pw.x = sa == -INFINITY ? 0.f : pw.x;
           pw.y = sb == -INFINITY ? 0.f : pw.y;
         }
-        // (logits beyond 2^24 are whole numbers or coarser in fp32: a weight may then lie
-        // above 2^15 by the exponents' error, and must not become infinite)
-        pa[gr][2 * i + hr] = pack_f16x2_finite(pw.x, pw.y);
+        pa[gr][2 * i + hr] = pack_f16x2(pw.x, pw.y);
         if constexpr (kSplit || kLow) {
           const float2 kept = unpack2<__half>(pa[gr][2 * i + hr]);
-          (kLow ? pa[gr][2 * i + 1] : pl[gr][2 * i + hr]) = pack_f16x2_finite(pw.x - kept.x, pw.y - kept.y);
+          (kLow ? pa[gr][2 * i + 1] : pl[gr][2 * i + hr]) = pack_f16x2(pw.x - kept.x, pw.y - kept.y);
         } else if constexpr (kHalves == 1) {
           pa[gr][2 * i + 1] = 0u;
         }
@@ -504,19 +500,23 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
     fetch_scales(first);
     int chunk_tile = 0;  // the current tile's place in its chunk
 
-    // m and mv are references a little behind the running maxima of x and of
-    // x + log2 vs: they move only when a value lies more than 2^kSlack above, so
-    // most tiles need no reduction over a row and no rescaling.  p and the fp16
-    // weights p vs / 2^mv, with mv kLift below, then reach 2^(kSlack + kLift): within
-    // fp16's limit, and as far as can be from its smallest step.  (With mv at the maximum
+    // m and d are references a little behind the running maxima of x and of x - m +
+    // log2 vs: they move only when a value lies more than 2^kSlack above, so
+    // most tiles need no reduction over a row and no rescaling.  p then reaches
+    // 2^kSlack, and the fp16 weights p vs / 2^d, with d kLift below, 2^(kSlack + kLift): within
+    // fp16's limit, and as far as can be from its smallest step.  (With d at the maximum
     // a warp lost the keys 2^-25 below its heaviest: of 2^20 keys of one CTA, 2^-26 each
     // beside one of 1, a quarter of their sum.)
     constexpr float kSlack = 8.f, kLift = 7.f;
-    constexpr float kNone = -1.0e30f;  // nothing seen yet
-    float m[kHalves], mv[kHalves], lsum[kHalves];
+    constexpr float kNone = -3.0e38f;   // nothing seen yet
+    constexpr float kLowest = -1.0e30f; // no value of V but zeros yet
+    constexpr float kLarge = 65536.f;   // of m: x is off by less than 2^-8 below it
+    bool large = false;                 // some row's m lies above that (the same for the whole warp)
+    float m[kHalves], d[kHalves], lsum[kHalves];
 #pragma unroll
     for (int hr = 0; hr < kHalves; ++hr) {
-      m[hr] = mv[hr] = kNone;
+      m[hr] = kNone;
+      d[hr] = kLowest;
       lsum[hr] = 0.f;
     }
     float o[Cfg::kTilesN][4];
@@ -684,33 +684,44 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
           }
         }
       }
-      float mx[kHalves], vx[kHalves];  // this lane's largest x, largest x + log2 vs
-#pragma unroll
-      for (int hr = 0; hr < kHalves; ++hr) {
-#pragma unroll
-        for (int gr = 0; gr < Cfg::kGroups; ++gr) {
-          const float top = fmaxf(fmax3(s[2 * gr][2 * hr], s[2 * gr][2 * hr + 1], s[2 * gr + 1][2 * hr]),
-                                  s[2 * gr + 1][2 * hr + 1]) * f[hr][gr];
-          mx[hr] = gr == 0 ? top : fmaxf(mx[hr], top);
-          vx[hr] = gr == 0 ? top + lv[gr] : fmaxf(vx[hr], top + lv[gr]);
-        }
-      }
+      // a row's largest x in one group of 16 keys, of this lane's (a rounded product of
+      // its own, for m and for what is subtracted from it)
+      auto top = [&](int hr, int gr) {
+        return __fmul_rn(fmaxf(fmax3(s[2 * gr][2 * hr], s[2 * gr][2 * hr + 1], s[2 * gr + 1][2 * hr]), s[2 * gr + 1][2 * hr + 1]),
+                         f[hr][gr]);
+      };
       bool above = false;
 #pragma unroll
-      for (int hr = 0; hr < kHalves; ++hr) above = above || mx[hr] > m[hr] + kSlack || vx[hr] > mv[hr] + (kSlack + kLift);
+      for (int hr = 0; hr < kHalves; ++hr) {
+        float mx, vx;  // this lane's largest x - m, largest x - m + log2 vs
+#pragma unroll
+        for (int gr = 0; gr < Cfg::kGroups; ++gr) {
+          const float x = top(hr, gr) - m[hr];
+          mx = gr == 0 ? x : fmaxf(mx, x);
+          vx = gr == 0 ? x + lv[gr] : fmaxf(vx, x + lv[gr]);
+        }
+        above = above || mx > kSlack || vx > d[hr] + (kSlack + kLift);
+      }
       if (__any_sync(0xffffffffu, above)) {
+        large = false;
 #pragma unroll
         for (int hr = 0; hr < kHalves; ++hr) {
+          float mn = m[hr], vn = kLowest;
 #pragma unroll
-          for (int sh = 1; sh < 4; sh <<= 1) {
-            mx[hr] = fmaxf(mx[hr], __shfl_xor_sync(0xffffffffu, mx[hr], sh));
-            vx[hr] = fmaxf(vx[hr], __shfl_xor_sync(0xffffffffu, vx[hr], sh));
-          }
-          const float mn = fmaxf(m[hr], mx[hr]), vn = fmaxf(mv[hr], vx[hr] - kLift);
-          lsum[hr] *= ex2_approx(m[hr] - mn);
-          const float al = ex2_approx(mv[hr] - vn);
+          for (int gr = 0; gr < Cfg::kGroups; ++gr) mn = fmaxf(mn, top(hr, gr));
+#pragma unroll
+          for (int sh = 1; sh < 4; sh <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, sh));
+#pragma unroll
+          for (int gr = 0; gr < Cfg::kGroups; ++gr) vn = fmaxf(vn, top(hr, gr) - mn + lv[gr] - kLift);
+#pragma unroll
+          for (int sh = 1; sh < 4; sh <<= 1) vn = fmaxf(vn, __shfl_xor_sync(0xffffffffu, vn, sh));
+          const float down = m[hr] - mn, was = d[hr] + down;
+          vn = fmaxf(vn, was);
+          lsum[hr] *= ex2_approx(down);
+          const float al = ex2_approx(was - vn);
           m[hr] = mn;
-          mv[hr] = vn;
+          d[hr] = vn;
+          large = large || (fabsf(mn) > kLarge && mn != kNone);
 #pragma unroll
           for (int j = 0; j < Cfg::kTilesN; ++j) {
             o[j][2 * hr] *= al;
@@ -721,10 +732,11 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
             }
           }
         }
+        large = __any_sync(0xffffffffu, large);
       }
       uint32_t pa[Cfg::kGroups][4], pl[kSplit ? Cfg::kGroups : 1][4];
-      if (masked) tile_weights<Cfg::kGroups, kHalves, true, kSplit, kLow>(s, f, lv, m, mv, lsum, pa, pl);
-      else tile_weights<Cfg::kGroups, kHalves, false, kSplit, kLow>(s, f, lv, m, mv, lsum, pa, pl);
+      if (masked || large) tile_weights<Cfg::kGroups, kHalves, true, kSplit, kLow>(s, f, lv, m, d, lsum, pa, pl);
+      else tile_weights<Cfg::kGroups, kHalves, false, kSplit, kLow>(s, f, lv, m, d, lsum, pa, pl);
 
       // ---- O += P V
 #pragma unroll
@@ -777,7 +789,7 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
     }
     float* cm = reinterpret_cast<float*>(smem);            // [4][16] running max
     float* cl = cm + kKv8Warps * kKv8Rows;                 // [4][16] sums
-    float* cv = cl + kKv8Warps * kKv8Rows;                 // [4][16] O's units
+    float* cv = cl + kKv8Warps * kKv8Rows;                 // [4][16] O's units beside the maximum's
     float4* co4 = reinterpret_cast<float4*>(smem + 1024);  // [4][D / 16][2][32]: values 16 c + 4 tq ..+3 of rows g, g + 8
     if constexpr (kLow) {
 #pragma unroll
@@ -791,7 +803,7 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
       for (int hr = 0; hr < kHalves; ++hr) {
         cm[warp * 16 + g + 8 * hr] = m[hr] == kNone ? -INFINITY : m[hr];
         cl[warp * 16 + g + 8 * hr] = lsum[hr];
-        cv[warp * 16 + g + 8 * hr] = mv[hr] == kNone ? -INFINITY : mv[hr];
+        cv[warp * 16 + g + 8 * hr] = d[hr];
       }
     }
 #pragma unroll
@@ -803,8 +815,8 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
     }
     __syncthreads();
 
-    // Per row: M = max_w m_w, L = sum_w 2^(m_w - M) l_w; O = sum_w 2^(mv_w - M) O_w / L
-    // (2^(mv_w - M) <= the largest vs: finite), LSE = M + log2 L.
+    // Per row: M = max_w m_w, L = sum_w 2^(m_w - M) l_w; O = sum_w 2^(m_w - M + d_w) O_w / L
+    // (that power <= the largest vs: finite), LSE = M + log2 L.
     const int rows_here = min(kKv8Rows, rows_total - rg * kKv8Rows);
     const int64_t orow0 = (static_cast<int64_t>(b) * a.Hq + static_cast<int64_t>(hkv) * G) * a.Lq +
                           static_cast<int64_t>(rg) * kKv8Rows;
@@ -819,10 +831,10 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
       float L = 0.f, wt[kKv8Warps];
 #pragma unroll
       for (int w = 0; w < kKv8Warps; ++w) {
-        const float mw = cm[w * 16 + r], vw = cv[w * 16 + r];
+        const float mw = cm[w * 16 + r];
         // a warp whose maximum is -inf saw no key, or only NaN: its sum then says so
         L += mw == -INFINITY ? cl[w * 16 + r] : ex2_approx(mw - M) * cl[w * 16 + r];
-        wt[w] = vw == -INFINITY ? 0.f : ex2_approx(vw - (M == -INFINITY ? 0.f : M));
+        wt[w] = mw == -INFINITY ? 0.f : ex2_approx(mw - M + cv[w * 16 + r]);
       }
       const float inv = L == 0.f ? 0.f : 1.0f / L;
 #pragma unroll

@@ -103,3 +103,32 @@ def test_logits_of_millions_stay_finite(power, unit, rows, dtype):
             assert torch.isfinite(out).all() and (out.float() <= 64 * want).all() and (out.float() >= want / 64).all(), (step, frac)
             x = unit * (100.0 * 2 ** power + 7 * step)
             assert ((lse.double() - x).abs() <= 2.0 ** -20 * x + 11 + 4).all()
+
+
+@pytest.mark.parametrize("rows", [1, 16])
+@pytest.mark.parametrize("dtype,logit", [("bf16", s * 2.0 ** e) for e in (10, 14, 17, 20, 24, 30, 60, 110, 120) for s in (1, -1)] +
+                         [("fp16", s * 2.0 ** e) for e in (10, 14, 17, 20) for s in (1, -1)])
+@pytest.mark.parametrize("n,ctas", [(1, 1), (48, 1), (1024, 5)])
+def test_values_do_not_depend_on_the_logits_size(n, ctas, rows, dtype, logit):
+    """All keys alike, logits of any size: O is the mean of the values, whose blocks have
+    scales 2^-9 to 2^-3 apart, and LSE = logit + log2 n (parts of equal length: the LSE of a
+    part holds log2 n to its own rounding only).  The softmax weights are 1 / n but
+    for ex2 (2^-22) and log2 of V's scale (2^-21), and where rounded once for fp16's 2^-11;
+    2^-16 for fp32 sums and the merge (the module's other notes)."""
+    cache = skv.kv8_cache(1, 1, 1024, 64, 16)
+    cache.k.zero_()
+    cache.k[..., 0] = 100
+    cache.k_scale.fill_(1.0)
+    cache.v.random_(-127, 128, generator=torch.Generator(device="cuda").manual_seed(n))
+    cache.v_scale.copy_(2.0 ** (-9 + 6 * torch.rand(cache.v_scale.shape, generator=gen(n))))
+    q = torch.zeros(1, rows, 1, 64, dtype=DT[dtype], device="cuda")
+    q[..., 0] = (1.0 if logit > 0 else -1.0) * (2.0 ** 9 if dtype == "fp16" else abs(logit) / 2.0 ** 5)
+    scale = float(np.float32(logit / (float(q[0, 0, 0, 0]) * 100.0) * np.log(2.0)))
+    out, lse = skv.attn_splitkv_decode_kv8(q, cache, scale, kv_len=i32([n]), num_ctas=ctas)
+    v = values(cache.v, cache.v_scale, [n])[0, 0, :n]
+    want, size = v.mean(0), np.abs(v).mean(0)
+    weight = 2.0 ** -11 if dtype == "bf16" and rows > 8 else 0.0
+    tol = half_step(want, dtype) + (2.0 ** -20 + 2.0 ** -16 + weight) * size
+    assert np.all(np.abs(O.to_f64(out)[0, :, 0] - want) <= tol)
+    x = float(q[0, 0, 0, 0]) * 100.0 * scale * np.log2(np.e)
+    assert np.all(np.abs(O.to_f64(lse) - (x + np.log2(n))) <= 2.0 ** -21 * abs(x) + 2.0 ** -17)
