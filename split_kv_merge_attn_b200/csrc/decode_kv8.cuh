@@ -26,14 +26,14 @@
 // What bounds it: bytes at D = 64 and e4m3 (6.1 TB/s; a copy reaches 6.6), else the
 // latency of each warp's own chain of arrival, conversion, Q K^T, softmax and P V, with
 // the two warps a scheduler that registers allow.  At D = 128, int8, 32768 keys nothing
-// is saturated: issue 41%, tensor pipe 30%, DRAM 54%; of the 4.8 cycles between two
+// is saturated: issue 41%, tensor pipe 30%, DRAM 55%; of the 4.8 cycles between two
 // instructions of a warp 1.6 are fixed latencies of the instruction before, 0.8 waits
-// for loads and barriers, 0.4 for a busy pipe.  (Turning a code costs 1.25 (K) and 1.5
+// for loads and barriers, 0.3 for a busy pipe.  (Turning a code costs 1.25 (K) and 1.5
 // (V) lane instructions for int8, less for e4m3; tcgen05 would want 128 rows.)  Whole
 // calls, bf16 q, one row a head:
 //   D = 64,  B = 16, 16 / 16 heads, 16384 keys: e4m3 87.5 us (6.1 TB/s), int8 99.0 (5.4)
-//   D = 128, B = 2, 32 / 8 heads, 32768 keys:   e4m3 28.3 us (4.8 TB/s), int8 30.5 (4.4)
-//   D = 256, B = 1, 16 / 4 heads, 131072 keys:  e4m3 49.7 us (5.4 TB/s), int8 56.2 (4.8)
+//   D = 128, B = 2, 32 / 8 heads, 32768 keys:   e4m3 28.1 us (4.8 TB/s), int8 30.5 (4.4)
+//   D = 256, B = 1, 16 / 4 heads, 131072 keys:  e4m3 49.8 us (5.4 TB/s), int8 55.8 (4.8)
 //   D = 128, B = 1, 32 / 8 heads, 4096 keys:    e4m3 8.7 us, int8 8.9: latency
 // Of these about 5 us are the start, the four warps' combine and the merge launch: at
 // 4096 keys the decode over 16-bit keys, of fewer parts, takes 6.8 us (at 32768 keys,
