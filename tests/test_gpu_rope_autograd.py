@@ -136,3 +136,35 @@ def test_writing_in_place_is_seen_by_autograd():
     with torch.inference_mode():
         x = q.clone()
     assert skv.rope_apply(x, None, pos, f, q_out=x)[0] is x
+
+
+def test_forward_and_backward_captured():
+    """Both passes in one graph, replayed with new inputs, gradients and positions."""
+    q, k, gq, gk, pos, f = inputs("HND", 2, 40, 4, 2, 64, 64, "bf16")
+    q.requires_grad_()
+    k.requires_grad_()
+
+    def both():
+        y, z = skv.rope_apply(q, k, pos, f)
+        return (y.detach(), z.detach(), *torch.autograd.grad((y, z), (q, k), (gq, gk)))
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        both()
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = both()
+    for seed in (1, 2):
+        new = inputs("HND", 2, 40, 4, 2, 64, 64, "bf16", seed=seed)
+        with torch.no_grad():
+            for t, x in zip((q, k, gq, gk, pos), new):
+                t.copy_(x)
+        graph.replay()
+        torch.cuda.synchronize()
+        with torch.no_grad():
+            want = (*skv.rope_apply(q, k, pos, f), *skv.rope_apply(gq, gk, pos, f, inverse=True))
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
